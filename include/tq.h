@@ -340,6 +340,101 @@ TQ_API tq_status tq_attend(const tq_codec *kc, const tq_codec *vc, const void *q
                     const tq_compressed *V, void *workspace, size_t ws_bytes,
                     float *out, void *stream);
 
+/* Workspace bytes for tq_attend_prefix (depends on the current device's SM
+ * count).                                                                    */
+TQ_API tq_status tq_attend_prefix_workspace_size(const tq_codec *kc,
+                                   const tq_codec *vc, int B, int Hq, int Hkv,
+                                   int64_t Tp, int64_t T, size_t *bytes);
+
+/* Decode attention of a batch that shares a prefix: B sequences attend over
+ * the same Tp prefix keys (computed once for all: a prefix key is read and
+ * decoded for the whole batch, not once a sequence) and over the keys of their
+ * own, of which sequence b holds the first lens[b] of T slots.
+ *   q        [B][Hq][d] of `dtype`, contiguous
+ *   Kp, Vp   prefix, Hkv * Tp rows; (h_kv, t) is row h_kv * Tp + t.  May be
+ *            NULL when Tp = 0
+ *   K, V     own keys and values, B * Hkv * T rows as in tq_scores; rows at
+ *            t >= lens[b] are not read.  May be NULL when T = 0
+ *   lens     device [B] int32, 0 <= lens[b] <= T; NULL: all T.  A length
+ *            outside is clamped and recorded as code 4 in kc's error word
+ *   scale    as tq_attend (0 -> 1/sqrt(d))
+ *   out      [B][Hq][d] of `out_dtype`: softmax over both parts together,
+ *            values and QJL-corrected values as tq_attend.  A sequence without
+ *            keys (Tp = 0, lens[b] = 0) gets zeros
+ *   lse      NULL, or [B][Hq] fp32: ln sum_t exp(scale * logit) over both
+ *            parts, -inf without keys
+ * The result of a call does not depend on other calls, and the same call gives
+ * the same bits.  The logits, the exponentials' sums and the weighted values
+ * are accumulated in fp32.  d <= 256, Hq / Hkv <= 32, a value sketch of m <= 128
+ * (else TQ_ERR_UNSUPPORTED).  workspace: 16-byte aligned; calls that may
+ * overlap on the GPU need one each.                                          */
+TQ_API tq_status tq_attend_prefix(const tq_codec *kc, const tq_codec *vc,
+                    const void *q, tq_dtype dtype, int B, int Hq, int Hkv,
+                    float scale, int64_t Tp, const tq_compressed *Kp,
+                    const tq_compressed *Vp, int64_t T, const int32_t *lens,
+                    const tq_compressed *K, const tq_compressed *V,
+                    void *workspace, size_t ws_bytes, void *out,
+                    tq_dtype out_dtype, float *lse, void *stream);
+
+/* Accumulated attention weight of every cached key, the statistic by which a
+ * bounded cache is kept: for sequence b, KV head k and t < lens[b]
+ *   mass[b][k][t] = decay * mass[b][k][t]
+ *                   + sum over the query heads h of k of p(b, h, t),
+ *   p = exp(scale * logits[b][h][t] - lse[b][h]).
+ *   logits   [B][Hq][T] fp32 as tq_scores writes them (unscaled); entries at
+ *            t >= lens[b] are not read
+ *   lens     device [B] int32 as in tq_attend_prefix; NULL: all T
+ *   lse      [B][Hq] fp32: the softmax's statistic over all of the row's keys,
+ *            such as tq_attend_prefix's lse when there is a shared prefix;
+ *            -inf adds nothing.  NULL: the softmax over the row's own lens[b]
+ *            keys; a row whose logits are all -inf adds nothing
+ *   scale    0 -> 1/sqrt(d) of kc
+ *   decay    finite; 1 keeps the sum, less than 1 lets old weight fade
+ *   mass     [B][Hkv][T] fp32, updated in place; entries at t >= lens[b] are
+ *            left as they were
+ * Hq / Hkv <= 32.                                                            */
+TQ_API tq_status tq_mass_update(const tq_codec *kc, const float *logits, int B,
+                    int Hq, int Hkv, int64_t T, const int32_t *lens,
+                    const float *lse, float scale, float decay, float *mass,
+                    void *stream);
+
+/* Choice of the keys that a bounded cache keeps, per sequence and KV head.
+ * With n = lens[b] (NULL: T) keys held:
+ *   n <= keep : all of them;
+ *   n > keep  : the first `sink`, the last `recent`, and of the others the
+ *               keep - sink - recent with the greatest mass (equal mass: the
+ *               lower index; NaN counts as less than every number).
+ *   mass     [B][Hkv][T] fp32
+ *   idx      [B][Hkv][keep] int32 out: the kept t in ascending order, -1
+ *            behind the last (the source list of tq_copy_rows)
+ *   mass_out NULL, or [B][Hkv][keep] fp32: the kept keys' mass, 0 behind the
+ *            last; not `mass` itself
+ *   lens_out NULL, or [B] int32: min(n, keep); not `lens` itself
+ * 1 <= keep, sink + recent <= keep; keep may exceed T.                       */
+TQ_API tq_status tq_evict_select(const tq_codec *kc, const float *mass, int B,
+                    int Hkv, int64_t T, const int32_t *lens, int64_t keep,
+                    int64_t sink, int64_t recent, int32_t *idx,
+                    float *mass_out, int32_t *lens_out, void *stream);
+
+/* Copy compressed records between two caches of one codec, `rows` blocks of
+ * src_T and dst_T records (rows = B * Hkv for the caches of tq_attend_prefix):
+ * for r < rows, i < n, record r * src_T + src_idx[r][i] of src is written to
+ * record r * dst_T + dst_idx[r][i] of dst.
+ *   src_idx, dst_idx  device [rows][n] int32; NULL: i itself (then n must not
+ *            exceed that cache's records per block).  -1 in either list skips
+ *            the record; any other index outside the block also does, and is
+ *            recorded as code 5 in the codec's error word.  The entries of a
+ *            block's dst_idx must differ (-1 apart)
+ * Records that no entry names are left as they were.  src and dst must not
+ * overlap.  With tq_evict_select's idx as src_idx it compacts a cache; with
+ * src_T = n = 1 and the lengths as dst_idx it appends freshly quantised rows to
+ * ragged sequences (every record has a fixed size and address, FibQuant page,
+ * section 1).                                                                */
+TQ_API tq_status tq_copy_rows(const tq_codec *codec, const tq_compressed *src,
+                    int64_t src_T, const tq_compressed *dst, int64_t dst_T,
+                    int64_t rows, int64_t n, const int32_t *src_idx,
+                    const int32_t *dst_idx, void *stream);
+
 /* Workspace bytes for tq_search_topk with nq queries and top-k (k >= 1). */
 TQ_API tq_status tq_search_workspace_size(const tq_codec *codec, int nq, int k,
                                           size_t *bytes);
@@ -367,8 +462,9 @@ TQ_API tq_status tq_search_topk(const tq_codec *codec, const void *q, tq_dtype d
  * completion give up after a bounded time (about two seconds), record a
  * nonzero code in the codec's device error word and return early.  This call
  * synchronises `stream`, reads the word into *code (0 = healthy, 1 = an MMA
- * completion wait timed out, 2 = a copy wait timed out), clears it, and
- * returns TQ_ERR_DEVICE_ASSERT if it was set.                                */
+ * completion wait timed out, 2 = a copy wait timed out, 3 = a RoPE position, 4 =
+ * a length, 5 = a record index out of range; the highest if several), clears
+ * it, and returns TQ_ERR_DEVICE_ASSERT if it was set.                        */
 TQ_API tq_status tq_codec_device_error(const tq_codec *codec, void *stream,
                                        uint32_t *code);
 

@@ -72,6 +72,11 @@ def _load() -> ctypes.CDLL:
         "tq_scores_noalloc": [P, P, I, I, I, I, I64, P, P, P],
         "tq_attend_workspace_size": [P, P, I, I, I, I64, ctypes.POINTER(SZ)],
         "tq_attend": [P, P, P, I, I, I, I, I64, ctypes.c_float, P, P, P, SZ, P, P],
+        "tq_attend_prefix_workspace_size": [P, P, I, I, I, I64, I64, ctypes.POINTER(SZ)],
+        "tq_attend_prefix": [P, P, P, I, I, I, I, ctypes.c_float, I64, P, P, I64, P, P, P, P, SZ, P, I, P, P],
+        "tq_mass_update": [P, P, I, I, I, I64, P, P, ctypes.c_float, ctypes.c_float, P, P],
+        "tq_evict_select": [P, P, I, I, I64, P, I64, I64, I64, P, P, P, P],
+        "tq_copy_rows": [P, P, I64, P, I64, I64, I64, P, P, P],
         "tq_search_workspace_size": [P, I, I, ctypes.POINTER(SZ)],
         "tq_search_topk": [P, P, I, I, P, I64, I, P, P, P, SZ, P],
         "tq_codec_device_error": [P, P, ctypes.POINTER(ctypes.c_uint32)],
@@ -311,6 +316,101 @@ def tq_attend(kc: Codec, vc: Codec, q: torch.Tensor, B: int, Hq: int, Hkv: int, 
                           workspace.numel() * workspace.element_size(), out.data_ptr(), _stream(stream)),
            "tq_attend")
     return out
+
+
+def _arg(t: Optional[torch.Tensor], name: str, codec: Codec, dtype, n: int) -> Optional[int]:
+    """Pointer of an optional tensor argument: contiguous, of `dtype`, of at
+    least n elements, on the codec's device."""
+    if t is None:
+        return None
+    assert t.dtype == dtype, f"{name} must be {dtype} (got {t.dtype})"
+    assert t.is_contiguous(), f"{name} must be contiguous"
+    assert t.numel() >= n, f"{name} has {t.numel()} elements, {n} needed"
+    assert t.is_cuda and t.device.index == codec.device, f"{name} must be on the codec's device"
+    return t.data_ptr()
+
+
+def _cache_arg(c: Optional[Compressed], name: str, codec: Codec, n: int):
+    """tq_compressed of an optional cache of at least n records."""
+    if c is None:
+        assert n == 0, f"{name} is missing"
+        return None
+    _arg(c.codes, name + ".codes", codec, torch.int32, n * codec.code_words)
+    _arg(c.norms, name + ".norms", codec, torch.float32, n)
+    if codec.m:
+        assert c.signs is not None and c.rnorms is not None, f"{name} lacks the codec's sketch"
+        _arg(c.signs, name + ".signs", codec, torch.int32, n * codec.sign_words)
+        _arg(c.rnorms, name + ".rnorms", codec, torch.float32, n)
+    return c.struct()
+
+
+def _ref(st):
+    return None if st is None else ctypes.byref(st)
+
+
+def tq_attend_prefix_workspace_size(kc: Codec, vc: Codec, B: int, Hq: int, Hkv: int, Tp: int, T: int) -> int:
+    v = ctypes.c_size_t()
+    _check(_lib.tq_attend_prefix_workspace_size(kc.handle, vc.handle, B, Hq, Hkv, Tp, T, ctypes.byref(v)),
+           "tq_attend_prefix_workspace_size")
+    return v.value
+
+
+def tq_attend_prefix(kc: Codec, vc: Codec, q: torch.Tensor, B: int, Hq: int, Hkv: int, Tp: int,
+                     Kp: Optional[Compressed], Vp: Optional[Compressed], T: int, K: Optional[Compressed],
+                     V: Optional[Compressed], out: torch.Tensor, workspace: torch.Tensor,
+                     lens: Optional[torch.Tensor] = None, scale: float = 0.0, lse: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Decode attention over Tp prefix keys that the batch shares and the first
+    lens[b] (int32; None: all) of T keys of each sequence's own; out in its own
+    dtype, lse [B, Hq] fp32 if given."""
+    ks, vs = _cache_arg(Kp, "Kp", kc, Hkv * Tp), _cache_arg(Vp, "Vp", vc, Hkv * Tp)
+    ko, vo = _cache_arg(K, "K", kc, B * Hkv * T), _cache_arg(V, "V", vc, B * Hkv * T)
+    _check(_lib.tq_attend_prefix(kc.handle, vc.handle, _arg(q, "q", kc, q.dtype, B * Hq * kc.d), _DTYPES[q.dtype], B,
+                                 Hq, Hkv, scale, Tp, _ref(ks), _ref(vs), T, _arg(lens, "lens", kc, torch.int32, B),
+                                 _ref(ko), _ref(vo), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(),
+                                 _arg(out, "out", kc, out.dtype, B * Hq * kc.d), _DTYPES[out.dtype],
+                                 _arg(lse, "lse", kc, torch.float32, B * Hq), _stream(stream)), "tq_attend_prefix")
+    return out
+
+
+def tq_mass_update(kc: Codec, logits: torch.Tensor, B: int, Hq: int, Hkv: int, T: int, mass: torch.Tensor,
+                   lens: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, scale: float = 0.0,
+                   decay: float = 1.0, stream=None) -> torch.Tensor:
+    """mass [B, Hkv, T] = decay * mass + the softmax weight of every key, summed
+    over its query heads, from tq_scores' logits [B, Hq, T] (in place)."""
+    _check(_lib.tq_mass_update(kc.handle, _arg(logits, "logits", kc, torch.float32, B * Hq * T), B, Hq, Hkv, T,
+                               _arg(lens, "lens", kc, torch.int32, B), _arg(lse, "lse", kc, torch.float32, B * Hq),
+                               scale, decay, _arg(mass, "mass", kc, torch.float32, B * Hkv * T), _stream(stream)),
+           "tq_mass_update")
+    return mass
+
+
+def tq_evict_select(kc: Codec, mass: torch.Tensor, B: int, Hkv: int, T: int, keep: int, idx: torch.Tensor,
+                    lens: Optional[torch.Tensor] = None, sink: int = 0, recent: int = 0,
+                    mass_out: Optional[torch.Tensor] = None, lens_out: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """The `keep` keys that stay of each (sequence, KV head): idx int32
+    [B, Hkv, keep], ascending, -1 behind the last."""
+    n = B * Hkv * max(keep, 0)
+    _check(_lib.tq_evict_select(kc.handle, _arg(mass, "mass", kc, torch.float32, B * Hkv * T), B, Hkv, T,
+                                _arg(lens, "lens", kc, torch.int32, B), keep, sink, recent,
+                                _arg(idx, "idx", kc, torch.int32, n),
+                                _arg(mass_out, "mass_out", kc, torch.float32, n),
+                                _arg(lens_out, "lens_out", kc, torch.int32, B), _stream(stream)), "tq_evict_select")
+    return idx
+
+
+def tq_copy_rows(codec: Codec, src: Compressed, src_T: int, dst: Compressed, dst_T: int, rows: int, n: int,
+                 src_idx: Optional[torch.Tensor] = None, dst_idx: Optional[torch.Tensor] = None,
+                 stream=None) -> Compressed:
+    """Copy record src_idx[r][i] of block r of src to record dst_idx[r][i] of
+    block r of dst (None: i itself; -1: skip)."""
+    ss, ds = _cache_arg(src, "src", codec, rows * src_T), _cache_arg(dst, "dst", codec, rows * dst_T)
+    _check(_lib.tq_copy_rows(codec.handle, _ref(ss), src_T, _ref(ds), dst_T, rows, n,
+                             _arg(src_idx, "src_idx", codec, torch.int32, rows * n),
+                             _arg(dst_idx, "dst_idx", codec, torch.int32, rows * n), _stream(stream)), "tq_copy_rows")
+    return dst
 
 
 def tq_search_workspace_size(codec: Codec, nq: int, k: int) -> int:
