@@ -72,9 +72,29 @@ int chunks_of(int64_t units, int64_t n, int sms) {
   return (int)std::max<int64_t>(std::max<int64_t>(want, 1), (n + 1023) / 1024);
 }
 
-tq_prefix_plan plan_of(int B, int Hq, int Hkv, int64_t Tp, int64_t T, int sms) {
+// The tensor-core kernel runs one block an SM, each with the rows of one group
+// (128 / G sequences of a KV head) and an equal share of its tiles: as many
+// blocks as fit in one wave, or, with more groups than SMs, the split of each
+// group that wastes the least of its last wave.
+tq_prefix_plan plan_of(const tq_params& kp, const tq_params& vp, int B, int Hq, int Hkv, int64_t Tp, int64_t T,
+                       int sms) {
   const int G = Hq / Hkv;
   tq_prefix_plan pl = {};
+  pl.tc = tq_prefix_tc_supported(kp, vp);
+  if (pl.tc) {
+    const int SB = 128 / G;
+    const int64_t groups = (int64_t)Hkv * ((B + SB - 1) / SB);
+    const int64_t tiles = (Tp + 63) / 64 + (T + 63) / 64 * std::min(B, SB);
+    if (groups == 0 || tiles == 0) return pl;
+    int64_t best = std::max<int64_t>(1, sms / groups);
+    if (groups > sms) {
+      auto waves = [&](int64_t n) { return (double)((groups * n + sms - 1) / sms) / (double)n; };
+      for (int64_t n = 2; n <= 4; ++n)
+        if (waves(n) < 0.95 * waves(best)) best = n;
+    }
+    pl.nP = (int)std::min(best, tiles);
+    return pl;
+  }
   pl.nP = chunks_of((int64_t)Hkv * (((int64_t)B * G + 7) / 8), Tp, sms);
   pl.nO = chunks_of((int64_t)B * Hkv * ((G + 7) / 8), T, sms);
   return pl;
@@ -106,7 +126,7 @@ extern "C" tq_status tq_attend_prefix_workspace_size(const tq_codec* kc, const t
   if (!kc || !vc || !bytes) return tq_fail(TQ_ERR_INVALID_ARG, "%s: null argument", name);
   tq_status st = prefix_shape(kc, vc, B, Hq, Hkv, Tp, T, name);
   if (st != TQ_OK) return st;
-  const tq_prefix_plan pl = plan_of(B, Hq, Hkv, Tp, T, sms_of(kc->device < 0 ? 0 : kc->device));
+  const tq_prefix_plan pl = plan_of(kc->p, vc->p, B, Hq, Hkv, Tp, T, sms_of(kc->device < 0 ? 0 : kc->device));
   *bytes = prefix_bytes(kc->p, vc->p, (int64_t)B * Hq, pl);
   return TQ_OK;
 }
@@ -132,7 +152,8 @@ extern "C" tq_status tq_attend_prefix(const tq_codec* kc, const tq_codec* vc, co
   if (lens && !aligned(lens, 4)) return tq_fail(TQ_ERR_INVALID_ARG, "%s: lens not 4-byte aligned", name);
   if (Tp > 0 && ((st = rows_ok(kc, Kp, name, "Kp")) != TQ_OK || (st = rows_ok(vc, Vp, name, "Vp")) != TQ_OK)) return st;
   if (T > 0 && ((st = rows_ok(kc, K, name, "K")) != TQ_OK || (st = rows_ok(vc, V, name, "V")) != TQ_OK)) return st;
-  const tq_prefix_plan pl = plan_of(B, Hq, Hkv, Tp, T, sms_of(kc->device));
+  tq_prefix_plan pl = plan_of(kc->p, vc->p, B, Hq, Hkv, Tp, T, sms_of(kc->device));
+  pl.split = out_dtype != TQ_BF16 || lse != nullptr;
   const int64_t rows = (int64_t)B * Hq;
   const size_t need = prefix_bytes(kc->p, vc->p, rows, pl);
   if (!aligned(workspace, 16) || ws_bytes < need)
@@ -152,7 +173,8 @@ extern "C" tq_status tq_attend_prefix(const tq_codec* kc, const tq_codec* vc, co
   a.qprep = (const float*)workspace;
   a.partials = (float*)((char*)workspace + qprep_size(kc->p, rows));
   cudaError_t e = tq_launch_qprep(kc->p, q, dt, (int)rows, (float*)workspace, s);
-  if (e == cudaSuccess) e = tq_launch_prefix_any(kc->p, vc->p, a, pl, s);
+  if (e == cudaSuccess && pl.nP + pl.nO > 0)
+    e = pl.tc ? tq_launch_prefix_tc(kc->p, vc->p, a, pl, s) : tq_launch_prefix_any(kc->p, vc->p, a, pl, s);
   if (e == cudaSuccess) e = tq_launch_prefix_combine(vc->p, a, pl, out, out_dtype, lse, s);
   return done(e, name);
 }

@@ -12,8 +12,8 @@ enum : uint32_t { kErrLength = 4, kErrRowIndex = 5 };
 // (sequence, KV head)'s own keys; each is cut into a fixed number of chunks,
 // and every (query row, chunk) leaves a partial (acc[d], max, sum[, a[m_v]]).
 struct tq_prefix_plan {
-  int nP;  // chunks per prefix unit (0: no prefix)
-  int nO;  // chunks per own unit (0: no own keys)
+  int nP;      // chunks per prefix unit (0: no prefix); tc: blocks per group of rows
+  int nO;      // chunks per own unit (0: no own keys, or tc)
   bool tc;     // tensor-core kernel (tq_prefix_tc.cu)
   bool split;  // its operands in two fp16 parts each
 };
@@ -30,6 +30,10 @@ struct tq_prefix_args {
 
 cudaError_t tq_launch_prefix_any(const tq_params& kp, const tq_params& vp, const tq_prefix_args& a,
                                  const tq_prefix_plan& plan, cudaStream_t st);
+// whether the codecs have the tensor-core kernel, and its launch
+bool tq_prefix_tc_supported(const tq_params& kp, const tq_params& vp);
+cudaError_t tq_launch_prefix_tc(const tq_params& kp, const tq_params& vp, const tq_prefix_args& a,
+                                const tq_prefix_plan& plan, cudaStream_t st);
 cudaError_t tq_launch_prefix_combine(const tq_params& vp, const tq_prefix_args& a, const tq_prefix_plan& plan,
                                      void* out, tq_dtype out_dtype, float* lse, cudaStream_t st);
 

@@ -1,0 +1,676 @@
+// Shared-prefix decode attention on the tensor cores (kind::f16 tcgen05.mma),
+// for scalar codes at d = 64 and 128, key sketches of m <= 128 and values
+// without a sketch.
+//
+// The rows of a block are the query heads of one KV head over SB = 128 / G
+// sequences: SB * G rows of an M = 128 tile.  Their keys are a list of tiles
+// of 64: the prefix's tiles, which serve every row, then each sequence's own,
+// which serve its G rows.  The list is cut into equal ranges, one per block;
+// a block keeps its queries, walks its range, carries for each row the running
+// maximum M, Z = sum 2^(l - M) and acc = sum 2^(l - M) v of the tiles that
+// serve it, and leaves one partial per row.  A prefix key is so decoded once
+// for 128 rows instead of once a query.
+//
+// Per tile, with c the centroids, s the signs, w = S q':
+//   S = q' c^T (64 columns) and R = w s^T (64 more) into TMEM,
+//   l = a_k S + b_k R,  a_k = nu scale log2(e) / sqrt(d), b_k = nu gamma coef scale log2(e)
+//   P = 2^(l - M) nu_v 2^(14 - e) as fp16, back into TMEM over S,
+//   O = P c_v into TMEM, added into acc in registers with the weight 2^(e - 14).
+// 2^e bounds the tile's value norms, so that P uses fp16's range whatever the
+// norms; O starts from zero each tile, so that the tensor core's truncating
+// accumulation only ever spans one tile.
+//
+// SPLIT: operands as two fp16 parts each (x = hi + lo, 2^-22 relative) and the
+// three products that matter, hi hi + hi lo + lo hi, the small ones first.
+// Taken for fp32 and fp16 results and where the softmax's statistics are asked
+// for; a bf16 result (half a step 2^-8) comes from one product of fp16
+// operands (half a step 2^-11).
+//
+// Operand bytes come from byte permutes: a code of up to three bits is a prmt
+// selector into the eight low or high bytes of the codebook's fp16 values; the
+// top bit of a 4-bit code is the sign of a symmetric codebook.  Selector word s
+// of a 32-coordinate group holds the codes of coordinates s + 4 j in nibble j,
+// so operand position 8 s + j of a group is coordinate s + 4 j; queries and the
+// output columns use the same order.
+//
+// Warps: 0-3 softmax (a thread a row), 4-11 accumulation (a thread half a
+// row's columns), 12-15 expansion of keys and values, 16 MMA issue.
+#include <math.h>
+
+#include <algorithm>
+
+#include "tq_cache.h"
+#include "tq_common.cuh"
+#include "tq_tc.cuh"
+
+namespace {
+
+constexpr int kKeys = 64;    // keys of a tile
+constexpr int kRows = 128;   // rows of a block
+constexpr int kThreads = 544;
+constexpr int kAccWarp0 = 4, kExpWarp0 = 12, kMmaWarp = 16;
+constexpr float kCenScale = 16.f;  // centroids as fp16: keeps the low parts out of the subnormals
+constexpr uint32_t kColO = 256, kColQ = 384;
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two floats to fp16x2 (lo in the low half), and back
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
+
+// coordinate of operand position p
+__host__ __device__ constexpr int coord_of(int p) { return (p & ~31) + ((p & 31) >> 3) + 4 * (p & 7); }
+// sketch row of operand position p
+__host__ __device__ constexpr int sketch_of(int p) { return (p & ~31) + ((p & 31) >> 1) + 16 * (p & 1); }
+
+// prmt tables of one segment: bytes of the fp16 high and low parts
+struct Tab {
+  uint32_t hl[2], hh[2], ll[2], lh[2];
+};
+
+struct Smem {
+  Tab tab[2][2];  // [keys, values][segment]
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], sdone[2], ofull, oempty, qfull, done;
+  uint32_t tmem;
+  int abort;
+  float a[2][kKeys], b[2][kKeys], c[2][kKeys], v[2][kKeys];  // per key: see the top
+  float f[8];                                                // 2^(e - 14) of a tile
+  float mrow[4][kRows];                                      // running maximum after a tile
+  int64_t len[kRows];                                        // keys of the block's sequences
+};
+
+template <int D, bool SPLIT>
+struct Layout {
+  static constexpr int NP = SPLIT ? 2 : 1;              // fp16 parts of an operand
+  static constexpr int kpart = kKeys * D * 2;           // one part of a key or value tile
+  static constexpr int VST = SPLIT ? 1 : 2;             // value stages
+  int w, k, sg, v, total, kstage;
+  __host__ __device__ explicit Layout(int m) {
+    w = 0;                                // W image: NP parts of [m / 8][128][16 bytes]
+    const int wpart = kRows * m * 2;
+    k = w + NP * wpart;                   // two key stages: centroid parts, then signs
+    sg = NP * kpart;                      // offset of the signs in a key stage
+    kstage = sg + kKeys * m * 2;
+    v = k + 2 * kstage;
+    total = v + VST * NP * kpart;
+  }
+};
+
+// 32 coordinates of one key from their bit planes: 4 chunks of 16 bytes at
+// `dst` + 1024 s (and the low parts at dst + lo_off)
+template <int P, bool SPLIT>
+__device__ __forceinline__ void expand32(const uint32_t (&pl)[4], const Tab& t, unsigned char* dst, int lo_off) {
+  uint32_t w[3];
+#pragma unroll
+  for (int p = 0; p < 3; ++p) w[p] = p < P ? (P == 4 ? ~(pl[p] ^ pl[3]) : pl[p]) : 0u;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    uint32_t sel = 0u;
+#pragma unroll
+    for (int p = 0; p < (P < 3 ? P : 3); ++p) {
+      const uint32_t x = s >= p ? w[p] >> (s - p) : w[p] << (p - s);
+      sel |= x & (0x11111111u << p);
+    }
+    uint32_t neg = 0u;  // 4 in the nibble of a negative coordinate
+    if constexpr (P == 4) neg = (s >= 2 ? ~pl[3] >> (s - 2) : ~pl[3] << (2 - s)) & 0x44444444u;
+    uint4 hi, lo;
+    uint32_t* ph = reinterpret_cast<uint32_t*>(&hi);
+    uint32_t* pw = reinterpret_cast<uint32_t*>(&lo);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t sl = h ? sel >> 16 : sel;
+      uint32_t sg = 0u;
+      if constexpr (P == 4) sg = prmt(0u, 0x80808080u, h ? neg >> 16 : neg);
+      const uint32_t a = prmt(t.hl[0], t.hl[1], sl), b = prmt(t.hh[0], t.hh[1], sl) ^ sg;
+      ph[2 * h] = prmt(a, b, 0x5140);
+      ph[2 * h + 1] = prmt(a, b, 0x7362);
+      if constexpr (SPLIT) {
+        const uint32_t c = prmt(t.ll[0], t.ll[1], sl), e = prmt(t.lh[0], t.lh[1], sl) ^ sg;
+        pw[2 * h] = prmt(c, e, 0x5140);
+        pw[2 * h + 1] = prmt(c, e, 0x7362);
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + 1024 * s) = hi;
+    if constexpr (SPLIT) *reinterpret_cast<uint4*>(dst + 1024 * s + lo_off) = lo;
+  }
+}
+
+template <bool SPLIT>
+__device__ __forceinline__ void expand_group(int bits, const uint32_t (&pl)[4], const Tab& t, unsigned char* dst,
+                                             int lo_off) {
+  switch (bits) {
+    case 1: expand32<1, SPLIT>(pl, t, dst, lo_off); break;
+    case 2: expand32<2, SPLIT>(pl, t, dst, lo_off); break;
+    case 3: expand32<3, SPLIT>(pl, t, dst, lo_off); break;
+    default: expand32<4, SPLIT>(pl, t, dst, lo_off);
+  }
+}
+
+// plane words of one key's half row: NWH words per plane from `src`
+template <int NWH>
+__device__ __forceinline__ void load_planes(uint32_t (&r)[4][NWH], const uint32_t* __restrict__ src, int pw, int bits,
+                                            bool valid) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    if constexpr (NWH == 2) {
+      const uint2 x = (valid && p < bits) ? __ldg(reinterpret_cast<const uint2*>(src + p * pw)) : make_uint2(0u, 0u);
+      r[p][0] = x.x;
+      r[p][1] = x.y;
+    } else {
+      r[p][0] = (valid && p < bits) ? __ldg(src + p * pw) : 0u;
+    }
+  }
+}
+
+// The block's tiles: prefix tiles, then every sequence's own.
+struct Cursor {
+  int seq;      // -1: prefix
+  int64_t t0;   // first key
+  __device__ void start(const Smem& s, int64_t tile, int64_t Tp) {
+    const int64_t np = (Tp + kKeys - 1) / kKeys;
+    seq = -1;
+    if (tile < np) {
+      t0 = tile * kKeys;
+      return;
+    }
+    tile -= np;
+    for (seq = 0;; ++seq) {
+      const int64_t k = (s.len[seq] + kKeys - 1) / kKeys;
+      if (tile < k) break;
+      tile -= k;
+    }
+    t0 = tile * kKeys;
+  }
+  __device__ void next(const Smem& s, int64_t Tp) {
+    t0 += kKeys;
+    if (t0 < (seq < 0 ? Tp : s.len[seq])) return;
+    t0 = 0;
+    for (++seq; seq < kRows && s.len[seq] == 0; ++seq) {
+    }
+  }
+};
+
+template <int D, bool SPLIT, bool SK>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_tc_kernel(const tq_params kp, const tq_params vp, const tq_prefix_args A, const int nC, const int SB) {
+  using L = Layout<D, SPLIT>;
+  constexpr int NWH = D / 64;
+  extern __shared__ __align__(1024) unsigned char dyn[];
+  __shared__ Smem sm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const L lay(kp.m);
+  const int nrb = (A.B + SB - 1) / SB;
+  const int c = blockIdx.x % nC, rb = blockIdx.x / nC % nrb, h = blockIdx.x / nC / nrb;
+  const int b0 = rb * SB, nb = min(SB, A.B - b0), rows = nb * A.G;
+
+  // ---- prologue
+  if (tid < kRows) {
+    int64_t n = 0;
+    if (tid < nb && A.T > 0) {
+      n = A.lens ? __ldg(A.lens + b0 + tid) : A.T;
+      if (n < 0 || n > A.T) {
+        atomicMax(kp.err, (uint32_t)kErrLength);
+        n = n < 0 ? 0 : A.T;
+      }
+    }
+    sm.len[tid] = n;
+  }
+  if (tid >= 128 && tid < 132) {
+    const int which = (tid - 128) >> 1, s = tid & 1;
+    const tq_params& p = which ? vp : kp;
+    Tab t = {};
+    if (s < p.nseg) {
+      for (int e = 0; e < 8; ++e) {
+        const int code = p.bits[s] == 4 ? 8 + e : e;
+        const float x = code < (1 << p.bits[s]) ? p.cen[s][code] * kCenScale : 0.f;
+        const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
+        const uint32_t uh = __half_as_ushort(hi), ul = __half_as_ushort(lo);
+        t.hl[e >> 2] |= (uh & 255u) << (8 * (e & 3));
+        t.hh[e >> 2] |= (uh >> 8) << (8 * (e & 3));
+        t.ll[e >> 2] |= (ul & 255u) << (8 * (e & 3));
+        t.lh[e >> 2] |= (ul >> 8) << (8 * (e & 3));
+      }
+    }
+    sm.tab[which][s] = t;
+  }
+  if (tid == 160) {
+    for (int i = 0; i < 2; ++i) {
+      tqtc::mbar_init(&sm.kfull[i], 128);
+      tqtc::mbar_init(&sm.kempty[i], 1);
+      tqtc::mbar_init(&sm.vfull[i], 128);
+      tqtc::mbar_init(&sm.vempty[i], 1);
+      tqtc::mbar_init(&sm.sfull[i], 1);
+      tqtc::mbar_init(&sm.pfull[i], 4);
+      tqtc::mbar_init(&sm.sdone[i], 4);
+    }
+    tqtc::mbar_init(&sm.ofull, 1);
+    tqtc::mbar_init(&sm.oempty, 8);
+    tqtc::mbar_init(&sm.qfull, 4);
+    tqtc::mbar_init(&sm.done, 1);
+    sm.abort = 0;
+    tqtc::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tqtc::tmem_alloc(&sm.tmem, 512);
+  tqtc::tc_fence_before();
+  __syncthreads();
+  tqtc::tc_fence_after();
+  const uint32_t tm = sm.tmem;
+  int64_t total = (A.Tp + kKeys - 1) / kKeys;
+  for (int i = 0; i < nb; ++i) total += (sm.len[i] + kKeys - 1) / kKeys;
+  const int64_t first = total * c / nC, last = total * (c + 1) / nC;
+  const int nt = (int)(last - first);
+  Cursor cur;
+  cur.seq = -1;
+  cur.t0 = 0;
+  if (nt > 0) cur.start(sm, first, A.Tp);
+  volatile int* abort = &sm.abort;
+  auto fail = [&]() {
+    atomicMax(kp.err, (uint32_t)tqtc::kErrMmaWait);
+    *abort = 1;
+  };
+  // a wait that gives up ends its role's loop, for a whole warp at a time
+#define WAIT_WARP(bar, parity)                                                               \
+  if (!__all_sync(TQ_FULL_MASK, tqtc::mbar_wait_or_abort(&(bar), (parity), abort))) {        \
+    fail();                                                                                  \
+    break;                                                                                   \
+  }
+#define WAIT_ONE(bar, parity)                                                                \
+  if (!tqtc::mbar_wait_or_abort(&(bar), (parity), abort)) {                                  \
+    fail();                                                                                  \
+    break;                                                                                   \
+  }
+
+  if (warp < 4) {
+    // ------------------------------------------------------------- softmax
+    const int r = tid;
+    const uint32_t lane_base = tm + ((uint32_t)(warp * 32) << 16);
+    const bool mine = r < rows;
+    const int qrow = mine ? (b0 + r / A.G) * A.Hq + h * A.G + r % A.G : 0;
+    const int myseq = mine ? r / A.G : -2;
+    const float* q = A.qprep + (size_t)qrow * (D + kp.m);
+    float rs = 1.f;
+    if (warp * 32 < rows && nt > 0) {
+      // the row's power-of-two scale: its largest element to [2^9, 2^10)
+      float mx = 0.f;
+      if (mine)
+        for (int i = 0; i < D + kp.m; i += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(q + i);
+          mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+        }
+      float up = 1.f;
+      if (mx > 0.f && mx < INFINITY) {
+        const int ex = max(-100, min(100, ilogbf(mx)));
+        up = ldexpf(1.f, 9 - ex);
+        rs = ldexpf(1.f, ex - 9);
+      }
+#pragma unroll 1
+      for (int g = 0; g < D / 32; ++g) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float x = mine ? q[coord_of(32 * g + 2 * i)] * up : 0.f, y = mine ? q[coord_of(32 * g + 2 * i + 1)] * up : 0.f;
+          hi[i] = pack_f16(x, y);
+          const float2 f = unpack_f16(hi[i]);
+          lo[i] = pack_f16(x - f.x, y - f.y);
+        }
+        tqtc::tmem_st16(lane_base + kColQ + 16 * g, hi);
+        if (SPLIT) tqtc::tmem_st16(lane_base + kColQ + D / 2 + 16 * g, lo);
+      }
+      tqtc::tmem_wait_st();
+      if (SK) {
+        const float* w = q + D;
+#pragma unroll 1
+        for (int ch = 0; ch < kp.m / 8; ++ch) {
+          uint4 hi, lo;
+          uint32_t* ph = reinterpret_cast<uint32_t*>(&hi);
+          uint32_t* pl = reinterpret_cast<uint32_t*>(&lo);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = mine ? w[sketch_of(8 * ch + 2 * i)] * up : 0.f, y = mine ? w[sketch_of(8 * ch + 2 * i + 1)] * up : 0.f;
+            ph[i] = pack_f16(x, y);
+            const float2 f = unpack_f16(ph[i]);
+            pl[i] = pack_f16(x - f.x, y - f.y);
+          }
+          unsigned char* dst = dyn + lay.w + ch * 2048 + (r >> 3) * 128 + (r & 7) * 16;
+          *reinterpret_cast<uint4*>(dst) = hi;
+          if (SPLIT) *reinterpret_cast<uint4*>(dst + kRows * kp.m * 2) = lo;
+        }
+        tqtc::fence_proxy_async_smem();
+      }
+    }
+    tqtc::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) tqtc::mbar_arrive(&sm.qfull);
+    float M = -INFINITY, Z = 0.f;
+    int j = 0;
+    for (; j < nt; ++j) {
+      const int s2 = j & 1, ph = (j >> 1) & 1;
+      WAIT_WARP(sm.sfull[s2], ph);
+      tqtc::tc_fence_after();
+      const bool act = mine && (cur.seq < 0 || cur.seq == myseq);
+      if (__any_sync(TQ_FULL_MASK, act)) {
+        float t[kKeys];
+        float mx = M;
+#pragma unroll
+        for (int k0 = 0; k0 < kKeys; k0 += 16) {
+          uint32_t x[16], y[16];
+          tqtc::tmem_ld16(lane_base + 128 * s2 + k0, x);
+          if (SK) tqtc::tmem_ld16(lane_base + 128 * s2 + 64 + k0, y);
+          tqtc::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float v = SK ? fmaf(sm.b[s2][k0 + i], __uint_as_float(y[i]), sm.c[s2][k0 + i]) : sm.c[s2][k0 + i];
+            v = fmaf(sm.a[s2][k0 + i], __uint_as_float(x[i]), v) * rs;
+            t[k0 + i] = v;
+            mx = fmaxf(mx, v);
+          }
+        }
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        float z = 0.f;
+#pragma unroll
+        for (int k0 = 0; k0 < kKeys; k0 += 32) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float p0 = ex2(t[k0 + 2 * i] - ref), p1 = ex2(t[k0 + 2 * i + 1] - ref);
+            z += p0 + p1;
+            const float x = p0 * sm.v[s2][k0 + 2 * i], y = p1 * sm.v[s2][k0 + 2 * i + 1];
+            hi[i] = pack_f16(x, y);
+            if (SPLIT) {
+              const float2 f = unpack_f16(hi[i]);
+              lo[i] = pack_f16(x - f.x, y - f.y);
+            }
+          }
+          tqtc::tmem_st16(lane_base + 128 * s2 + k0 / 2, hi);
+          if (SPLIT) tqtc::tmem_st16(lane_base + 128 * s2 + 32 + k0 / 2, lo);
+        }
+        tqtc::tmem_wait_st();
+        if (act) {
+          Z = fmaf(Z, M == -INFINITY ? 0.f : ex2(M - ref), z);
+          M = mx;
+        }
+      }
+      sm.mrow[j & 3][r] = M;
+      tqtc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        tqtc::mbar_arrive(&sm.sdone[s2]);
+        tqtc::mbar_arrive(&sm.pfull[s2]);
+      }
+      cur.next(sm, A.Tp);
+    }
+    if (mine) {
+      float* pr = A.partials + ((size_t)qrow * nC + c) * (D + 2);
+      pr[D] = M;
+      pr[D + 1] = Z;
+    }
+  } else if (warp < kExpWarp0) {
+    // -------------------------------------------------------- accumulation
+    const int quad = warp & 3, half = (warp - kAccWarp0) >> 2;
+    const int r = quad * 32 + lane;
+    const bool mine = r < rows;
+    const int myseq = mine ? r / A.G : -2;
+    constexpr int NCOL = D / 2;
+    const uint32_t o_base = tm + ((uint32_t)(quad * 32) << 16) + kColO + half * NCOL;
+    float acc[NCOL];
+#pragma unroll
+    for (int i = 0; i < NCOL; ++i) acc[i] = 0.f;
+    float M = -INFINITY;
+    for (int j = 0; j < nt; ++j) {
+      WAIT_WARP(sm.ofull, j & 1);
+      tqtc::tc_fence_after();
+      const bool act = mine && (cur.seq < 0 || cur.seq == myseq);
+      if (__any_sync(TQ_FULL_MASK, act)) {
+        const float m2 = sm.mrow[j & 3][r], f = sm.f[j & 7];
+        const float al = act ? (m2 == M ? 1.f : ex2(M - m2)) : 1.f;
+        if (__any_sync(TQ_FULL_MASK, al != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < NCOL; ++i) acc[i] *= al;
+        }
+        if (act) M = m2;
+#pragma unroll
+        for (int k0 = 0; k0 < NCOL; k0 += 16) {
+          uint32_t x[16];
+          tqtc::tmem_ld16(o_base + k0, x);
+          tqtc::tmem_wait_ld();
+          if (act) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[k0 + i] = fmaf(__uint_as_float(x[i]), f, acc[k0 + i]);
+          }
+        }
+      }
+      tqtc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tqtc::mbar_arrive(&sm.oempty);
+      cur.next(sm, A.Tp);
+    }
+    if (mine) {
+      const int qrow = (b0 + r / A.G) * A.Hq + h * A.G + r % A.G;
+      float* pr = A.partials + ((size_t)qrow * nC + c) * (D + 2);
+      const float k = vp.inv_sqrt_d / kCenScale;
+#pragma unroll
+      for (int i = 0; i < NCOL; ++i) pr[coord_of(half * NCOL + i)] = acc[i] * k;
+    }
+  } else if (warp < kMmaWarp) {
+    // ----------------------------------------------------------- expansion
+    const int te = tid - kExpWarp0 * 32, key = te & 63, half = te >> 6;
+    const int ks = kp.nseg == 2 ? half : 0, vs = vp.nseg == 2 ? half : 0;
+    const int kw0 = kp.segbase[ks] + (kp.nseg == 2 ? 0 : half * NWH), vw0 = vp.segbase[vs] + (vp.nseg == 2 ? 0 : half * NWH);
+    const int kbits = kp.bits[ks], vbits = vp.bits[vs];
+    const Tab tk = sm.tab[0][ks], tv = sm.tab[1][vs];
+    const int off = (key >> 3) * 128 + (key & 7) * 16;
+    uint32_t kw[4][NWH], vw[4][NWH], sg[2];
+    float nu = 0.f, gam = 0.f, nv0 = 0.f, nv1 = 0.f;
+    bool kvalid = false;
+    auto load_k = [&](const Cursor& cu) {
+      const bool pre = cu.seq < 0;
+      const int64_t n = pre ? A.Tp : sm.len[cu.seq];
+      const tq_compressed& K = pre ? A.Kp : A.K;
+      const tq_compressed& V = pre ? A.Vp : A.V;
+      const int64_t base = pre ? (int64_t)h * A.Tp : ((int64_t)(b0 + cu.seq) * A.Hkv + h) * A.T;
+      kvalid = cu.t0 + key < n;
+      const int64_t row = base + cu.t0 + key;
+      load_planes<NWH>(kw, K.codes + row * kp.W + kw0, kp.pw, kbits, kvalid);
+      if (SK) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sg[i] = (kvalid && half + 2 * i < kp.MS) ? __ldg(K.signs + row * kp.MS + half + 2 * i) : 0u;
+        gam = kvalid ? __ldg(K.rnorms + row) : 0.f;
+      }
+      nu = kvalid ? __ldg(K.norms + row) : 0.f;
+      // value norms of keys lane and lane + 32: every warp sees the whole tile
+      nv0 = cu.t0 + lane < n ? __ldg(V.norms + base + cu.t0 + lane) : 0.f;
+      nv1 = cu.t0 + 32 + lane < n ? __ldg(V.norms + base + cu.t0 + 32 + lane) : 0.f;
+    };
+    auto load_v = [&](const Cursor& cu) {
+      const bool pre = cu.seq < 0;
+      const int64_t n = pre ? A.Tp : sm.len[cu.seq];
+      const int64_t base = pre ? (int64_t)h * A.Tp : ((int64_t)(b0 + cu.seq) * A.Hkv + h) * A.T;
+      const bool valid = cu.t0 + key < n;
+      load_planes<NWH>(vw, (pre ? A.Vp : A.V).codes + (base + cu.t0 + key) * vp.W + vw0, vp.pw, vbits, valid);
+    };
+    Cursor ck = cur, cv = cur;
+    if (nt > 0) {
+      load_k(ck);
+      load_v(cv);
+    }
+    const float ca = A.scale_log2e * kp.inv_sqrt_d / kCenScale, cb = A.scale_log2e * kp.qjl_coef;
+    // keys of tile j, then the values of tile j - 1
+    for (int j = 0; j <= nt; ++j) {
+      if (j < nt) {
+        const int s2 = j & 1;
+        if (j >= 2) {
+          WAIT_WARP(sm.kempty[s2], ((j >> 1) & 1) ^ 1);
+          WAIT_WARP(sm.sdone[s2], ((j >> 1) & 1) ^ 1);
+        }
+        unsigned char* st = dyn + lay.k + s2 * lay.kstage;
+#pragma unroll
+        for (int i = 0; i < NWH; ++i) {
+          const uint32_t pl[4] = {kw[0][i], kw[1][i], kw[2][i], kw[3][i]};
+          expand_group<SPLIT>(kbits, pl, tk, st + (half * NWH + i) * 4096 + off, L::kpart);
+        }
+        if (SK) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int w = half + 2 * i;
+            if (w < kp.MS) {
+#pragma unroll
+              for (int ch = 0; ch < 4; ++ch) {
+                uint4 x;
+                x.x = ((sg[i] << (15 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
+                x.y = ((sg[i] << (14 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
+                x.z = ((sg[i] << (13 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
+                x.w = ((sg[i] << (12 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
+                *reinterpret_cast<uint4*>(st + lay.sg + (4 * w + ch) * 1024 + off) = x;
+              }
+            }
+          }
+        }
+        float nm = fmaxf(fabsf(nv0), fabsf(nv1));
+        nm = tq_warp_max(nm);
+        int e = 0;
+        if (nm > 0.f && nm < INFINITY) e = max(-100, ilogbf(nm) + 1);
+        const float dn = ldexpf(1.f, 14 - e);
+        if (half == 0) {
+          sm.a[s2][key] = nu * ca;
+          sm.b[s2][key] = nu * gam * cb;
+          sm.c[s2][key] = kvalid ? 0.f : -INFINITY;
+          sm.v[s2][key] = ((key & 32) ? nv1 : nv0) * dn;
+          if (key == 0) sm.f[j & 7] = ldexpf(1.f, e - 14);
+        }
+        tqtc::fence_proxy_async_smem();
+        tqtc::mbar_arrive(&sm.kfull[s2]);
+        if (j + 1 < nt) {
+          ck.next(sm, A.Tp);
+          load_k(ck);
+        }
+      }
+      if (j > 0) {
+        const int i0 = j - 1, sv = L::VST == 2 ? (i0 & 1) : 0, use = L::VST == 2 ? (i0 >> 1) : i0;
+        if (use >= 1) WAIT_WARP(sm.vempty[sv], (use & 1) ^ 1);
+        unsigned char* st = dyn + lay.v + sv * L::NP * L::kpart;
+#pragma unroll
+        for (int i = 0; i < NWH; ++i) {
+          const uint32_t pl[4] = {vw[0][i], vw[1][i], vw[2][i], vw[3][i]};
+          expand_group<SPLIT>(vbits, pl, tv, st + (half * NWH + i) * 4096 + off, L::kpart);
+        }
+        tqtc::fence_proxy_async_smem();
+        tqtc::mbar_arrive(&sm.vfull[sv]);
+        if (j < nt) {
+          cv.next(sm, A.Tp);
+          load_v(cv);
+        }
+      }
+    }
+  } else if (lane == 0 && nt > 0) {
+    // ----------------------------------------------------------- MMA issue
+    constexpr uint32_t idS = tqtc::instr_desc(1, 0, 0, 128, kKeys);
+    constexpr uint32_t idO = tqtc::instr_desc(1, 0, 0, 128, D) | (1u << 16);  // B with its N index contiguous
+    const uint32_t base = tqtc::smem_u32(dyn);
+    for (int j = 0; j <= nt; ++j) {
+      if (j < nt) {
+        const int s2 = j & 1, ph = (j >> 1) & 1;
+        if (j == 0) WAIT_ONE(sm.qfull, 0);
+        WAIT_ONE(sm.kfull[s2], ph);
+        tqtc::tc_fence_after();
+        const uint32_t dS = tm + 128 * s2, kst = base + lay.k + s2 * lay.kstage;
+        // parts: low queries, low keys, then the high product
+#pragma unroll
+        for (int pr = SPLIT ? 0 : 2; pr < 3; ++pr) {
+          const uint32_t qa = tm + kColQ + (pr == 0 ? D / 2 : 0), kb = kst + (pr == 1 ? L::kpart : 0);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tqtc::mma_f16_ts(dS, qa + 8 * k, tqtc::smem_desc(kb + 2048 * k, 1024, 128), idS,
+                             !(k == 0 && pr == (SPLIT ? 0 : 2)));
+        }
+        if (SK) {
+          for (int pr = SPLIT ? 0 : 1; pr < 2; ++pr) {
+            const uint32_t wa = base + lay.w + (pr == 0 ? kRows * kp.m * 2 : 0);
+            for (int k = 0; k < kp.m / 16; ++k)
+              tqtc::mma_f16_ss(dS + 64, tqtc::smem_desc(wa + 4096 * k, 2048, 128),
+                               tqtc::smem_desc(kst + lay.sg + 2048 * k, 1024, 128), idS,
+                               !(k == 0 && pr == (SPLIT ? 0 : 1)));
+          }
+        }
+        tqtc::mma_commit(&sm.kempty[s2]);
+        tqtc::mma_commit(&sm.sfull[s2]);
+      }
+      if (j > 0) {
+        const int i0 = j - 1, s2 = i0 & 1, ph = (i0 >> 1) & 1;
+        const int sv = L::VST == 2 ? s2 : 0, use = L::VST == 2 ? (i0 >> 1) : i0;
+        WAIT_ONE(sm.pfull[s2], ph);
+        WAIT_ONE(sm.vfull[sv], use & 1);
+        if (i0 >= 1) WAIT_ONE(sm.oempty, (i0 & 1) ^ 1);
+        tqtc::tc_fence_after();
+        const uint32_t dO = tm + kColO, pA = tm + 128 * s2, vst = base + lay.v + sv * L::NP * L::kpart;
+#pragma unroll
+        for (int pr = SPLIT ? 0 : 2; pr < 3; ++pr) {
+          const uint32_t pa = pA + (pr == 0 ? 32 : 0), vb = vst + (pr == 1 ? L::kpart : 0);
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            tqtc::mma_f16_ts(dO, pa + 8 * k, tqtc::smem_desc(vb + 256 * k, 128, 1024), idO,
+                             !(k == 0 && pr == (SPLIT ? 0 : 2)));
+        }
+        tqtc::mma_commit(&sm.vempty[sv]);
+        tqtc::mma_commit(&sm.ofull);
+      }
+    }
+    // every product and commit has landed before the block ends
+    tqtc::mma_commit(&sm.done);
+    if (!tqtc::mbar_wait(&sm.done, 0)) fail();
+  }
+#undef WAIT_WARP
+#undef WAIT_ONE
+  __syncwarp();
+  tqtc::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tqtc::tc_fence_after();
+    tqtc::tmem_dealloc(tm, 512);
+  }
+}
+
+template <int D, bool SPLIT, bool SK>
+cudaError_t launch(const tq_params& kp, const tq_params& vp, const tq_prefix_args& a, int nC, int SB, unsigned grid,
+                   cudaStream_t st) {
+  const Layout<D, SPLIT> lay(kp.m);
+  auto fn = prefix_tc_kernel<D, SPLIT, SK>;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, lay.total);
+  if (e != cudaSuccess) return e;
+  fn<<<grid, kThreads, lay.total, st>>>(kp, vp, a, nC, SB);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool tq_prefix_tc_supported(const tq_params& kp, const tq_params& vp) {
+  return (kp.d == 64 || kp.d == 128) && kp.m <= 128 && vp.m == 0 && !kp.vq_bits && !vp.vq_bits;
+}
+
+cudaError_t tq_launch_prefix_tc(const tq_params& kp, const tq_params& vp, const tq_prefix_args& a,
+                                const tq_prefix_plan& plan, cudaStream_t st) {
+  const int SB = kRows / a.G;
+  const int64_t grid = (int64_t)a.Hkv * ((a.B + SB - 1) / SB) * plan.nP;
+  if (grid > 0x7fffffffll) return cudaErrorNotSupported;
+  const unsigned g = (unsigned)grid;
+#define GO(DD, SS) \
+  return kp.m ? launch<DD, SS, true>(kp, vp, a, plan.nP, SB, g, st) : launch<DD, SS, false>(kp, vp, a, plan.nP, SB, g, st)
+  if (kp.d == 64) {
+    if (plan.split) GO(64, true);
+    GO(64, false);
+  }
+  if (plan.split) GO(128, true);
+  GO(128, false);
+#undef GO
+}
