@@ -33,8 +33,10 @@
 // so operand position 8 s + j of a group is coordinate s + 4 j; queries and the
 // output columns use the same order.
 //
-// Warps: 0-3 softmax (a thread a row), 4-11 accumulation (a thread half a
-// row's columns), 12-15 expansion of keys and values, 16 MMA issue.
+// Warpgroups: 0-1 softmax (a thread half a row's keys), 2-3 accumulation (a
+// thread half a row's columns), 4 expansion of keys, 5 of values, 6 MMA issue
+// (one warp).  Keys of tile j + 1 are expanded and multiplied while tile j is in
+// its softmax.
 #include <math.h>
 
 #include <algorithm>
@@ -47,8 +49,11 @@ namespace {
 
 constexpr int kKeys = 64;    // keys of a tile
 constexpr int kRows = 128;   // rows of a block
-constexpr int kThreads = 544;
-constexpr int kAccWarp0 = 4, kExpWarp0 = 12, kMmaWarp = 16;
+constexpr int kThreads = 896;
+constexpr int kAccWarp0 = 8, kKeyWarp0 = 16, kValWarp0 = 20, kMmaWarp = 24;
+// registers a thread after the roles have split the 72 of the launch:
+// 2 * 80 + 2 * 88 + 72 + 72 + 24 = 7 * 72
+constexpr int kRegSoft = 80, kRegAcc = 88, kRegMma = 24;
 constexpr float kCenScale = 16.f;  // centroids as fp16: keeps the low parts out of the subnormals
 constexpr uint32_t kColO = 256, kColQ = 384;
 
@@ -62,6 +67,51 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+typedef unsigned long long u64;
+__device__ __forceinline__ u64 pair(uint32_t lo, uint32_t hi) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ u64 pair(float x) { return pair(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ float2 parts(u64 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// one lane of a converged warp
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(addr)
+               : "memory");
+}
+// exponent e of x = f 2^e, 1 <= f < 2 (subnormals: -127; infinities: 0), and 2^e
+__device__ __forceinline__ int exponent_of(float x) {
+  const int e = (int)(__float_as_uint(x) >> 23 & 255u);
+  return e == 255 ? 0 : e - 127;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 <= e <= 127
 // two floats to fp16x2 (lo in the low half), and back
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -82,10 +132,12 @@ struct Tab {
 
 struct Smem {
   Tab tab[2][2];  // [keys, values][segment]
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], sdone[2], ofull, oempty, qfull, done;
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], pair[4], ofull, oempty, qfull, done;
   uint32_t tmem;
   int abort;
-  float a[2][kKeys], b[2][kKeys], c[2][kKeys], v[2][kKeys];  // per key: see the top
+  alignas(16) float a[4][kKeys], b[4][kKeys], v[4][kKeys];   // per key: a_k, b_k, nu_v 2^(14 - e)
+  float smax[2][2][kRows];                                   // a half tile's maximum
+  float zsum[2][kRows];
   float f[8];                                                // 2^(e - 14) of a tile
   float mrow[4][kRows];                                      // running maximum after a tile
   int64_t len[kRows];                                        // keys of the block's sequences
@@ -252,12 +304,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tqtc::mbar_init(&sm.vfull[i], 128);
       tqtc::mbar_init(&sm.vempty[i], 1);
       tqtc::mbar_init(&sm.sfull[i], 1);
-      tqtc::mbar_init(&sm.pfull[i], 4);
-      tqtc::mbar_init(&sm.sdone[i], 4);
+      tqtc::mbar_init(&sm.pfull[i], 8);
     }
+    for (int i = 0; i < 4; ++i) tqtc::mbar_init(&sm.pair[i], 2);
     tqtc::mbar_init(&sm.ofull, 1);
     tqtc::mbar_init(&sm.oempty, 8);
-    tqtc::mbar_init(&sm.qfull, 4);
+    tqtc::mbar_init(&sm.qfull, 8);
     tqtc::mbar_init(&sm.done, 1);
     sm.abort = 0;
     tqtc::fence_mbar_init();
@@ -286,168 +338,201 @@ __global__ void __launch_bounds__(kThreads, 1)
     fail();                                                                                  \
     break;                                                                                   \
   }
-#define WAIT_ONE(bar, parity)                                                                \
-  if (!tqtc::mbar_wait_or_abort(&(bar), (parity), abort)) {                                  \
-    fail();                                                                                  \
-    break;                                                                                   \
-  }
 
-  if (warp < 4) {
+  if (warp < kAccWarp0) {
     // ------------------------------------------------------------- softmax
-    const int r = tid;
-    const uint32_t lane_base = tm + ((uint32_t)(warp * 32) << 16);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoft));
+    const int quad = warp & 3, half = warp >> 2, r = quad * 32 + lane;
+    const uint32_t lane_base = tm + ((uint32_t)(quad * 32) << 16);
     const bool mine = r < rows;
     const int qrow = mine ? (b0 + r / A.G) * A.Hq + h * A.G + r % A.G : 0;
     const int myseq = mine ? r / A.G : -2;
     const float* q = A.qprep + (size_t)qrow * (D + kp.m);
-    float rs = 1.f;
-    if (warp * 32 < rows && nt > 0) {
+    float rs = 1.f, M = -INFINITY, Z = 0.f;
+    int turn = 0;  // phases of this quadrant's pair of warps
+    for (int once = 0; once < 1 && nt > 0; ++once) {
       // the row's power-of-two scale: its largest element to [2^9, 2^10)
-      float mx = 0.f;
-      if (mine)
-        for (int i = 0; i < D + kp.m; i += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(q + i);
-          mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
-        }
-      float up = 1.f;
-      if (mx > 0.f && mx < INFINITY) {
-        const int ex = max(-100, min(100, ilogbf(mx)));
-        up = ldexpf(1.f, 9 - ex);
-        rs = ldexpf(1.f, ex - 9);
-      }
-#pragma unroll 1
-      for (int g = 0; g < D / 32; ++g) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float x = mine ? q[coord_of(32 * g + 2 * i)] * up : 0.f, y = mine ? q[coord_of(32 * g + 2 * i + 1)] * up : 0.f;
-          hi[i] = pack_f16(x, y);
-          const float2 f = unpack_f16(hi[i]);
-          lo[i] = pack_f16(x - f.x, y - f.y);
-        }
-        tqtc::tmem_st16(lane_base + kColQ + 16 * g, hi);
-        if (SPLIT) tqtc::tmem_st16(lane_base + kColQ + D / 2 + 16 * g, lo);
-      }
-      tqtc::tmem_wait_st();
-      if (SK) {
-        const float* w = q + D;
-#pragma unroll 1
-        for (int ch = 0; ch < kp.m / 8; ++ch) {
-          uint4 hi, lo;
-          uint32_t* ph = reinterpret_cast<uint32_t*>(&hi);
-          uint32_t* pl = reinterpret_cast<uint32_t*>(&lo);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = mine ? w[sketch_of(8 * ch + 2 * i)] * up : 0.f, y = mine ? w[sketch_of(8 * ch + 2 * i + 1)] * up : 0.f;
-            ph[i] = pack_f16(x, y);
-            const float2 f = unpack_f16(ph[i]);
-            pl[i] = pack_f16(x - f.x, y - f.y);
+      if (quad * 32 < rows) {
+        float mx = 0.f;
+        if (mine)
+          for (int i = half ? D : 0; i < (half ? D + kp.m : D); i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(q + i);
+            mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
           }
-          unsigned char* dst = dyn + lay.w + ch * 2048 + (r >> 3) * 128 + (r & 7) * 16;
-          *reinterpret_cast<uint4*>(dst) = hi;
-          if (SPLIT) *reinterpret_cast<uint4*>(dst + kRows * kp.m * 2) = lo;
+        sm.smax[turn & 1][half][r] = mx;
+        __syncwarp();
+        if (lane == 0) tqtc::mbar_arrive(&sm.pair[quad]);
+        WAIT_WARP(sm.pair[quad], turn & 1);
+        mx = fmaxf(mx, sm.smax[turn & 1][half ^ 1][r]);
+        ++turn;
+        float up = 1.f;
+        if (mx > 0.f && mx < INFINITY) {
+          const int ex = max(-100, min(100, exponent_of(mx)));
+          up = pow2(9 - ex);
+          rs = pow2(ex - 9);
         }
-        tqtc::fence_proxy_async_smem();
+        if (half == 0) {
+#pragma unroll 1
+          for (int g = 0; g < D / 32; ++g) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float x = mine ? q[coord_of(32 * g + 2 * i)] * up : 0.f, y = mine ? q[coord_of(32 * g + 2 * i + 1)] * up : 0.f;
+              hi[i] = pack_f16(x, y);
+              const float2 f = unpack_f16(hi[i]);
+              lo[i] = pack_f16(x - f.x, y - f.y);
+            }
+            tqtc::tmem_st16(lane_base + kColQ + 16 * g, hi);
+            if (SPLIT) tqtc::tmem_st16(lane_base + kColQ + D / 2 + 16 * g, lo);
+          }
+          tqtc::tmem_wait_st();
+        } else if (SK) {
+          const float* w = q + D;
+#pragma unroll 1
+          for (int ch = 0; ch < kp.m / 8; ++ch) {
+            uint4 hi, lo;
+            uint32_t* ph = reinterpret_cast<uint32_t*>(&hi);
+            uint32_t* pl = reinterpret_cast<uint32_t*>(&lo);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float x = mine ? w[sketch_of(8 * ch + 2 * i)] * up : 0.f, y = mine ? w[sketch_of(8 * ch + 2 * i + 1)] * up : 0.f;
+              ph[i] = pack_f16(x, y);
+              const float2 f = unpack_f16(ph[i]);
+              pl[i] = pack_f16(x - f.x, y - f.y);
+            }
+            unsigned char* dst = dyn + lay.w + ch * 2048 + (r >> 3) * 128 + (r & 7) * 16;
+            *reinterpret_cast<uint4*>(dst) = hi;
+            if (SPLIT) *reinterpret_cast<uint4*>(dst + kRows * kp.m * 2) = lo;
+          }
+          tqtc::fence_proxy_async_smem();
+        }
       }
     }
     tqtc::tc_fence_before();
     __syncwarp();
     if (lane == 0) tqtc::mbar_arrive(&sm.qfull);
-    float M = -INFINITY, Z = 0.f;
-    int j = 0;
-    for (; j < nt; ++j) {
+    for (int j = 0; j < nt; ++j) {
       const int s2 = j & 1, ph = (j >> 1) & 1;
       WAIT_WARP(sm.sfull[s2], ph);
       tqtc::tc_fence_after();
       const bool act = mine && (cur.seq < 0 || cur.seq == myseq);
       if (__any_sync(TQ_FULL_MASK, act)) {
-        float t[kKeys];
-        float mx = M;
+        const uint32_t s_col = lane_base + 128 * s2;
+        const float* ka = sm.a[j & 3] + 32 * half;
+        const float* kb = sm.b[j & 3] + 32 * half;
+        const float* kv = sm.v[j & 3] + 32 * half;
+        u64 t[16];
 #pragma unroll
-        for (int k0 = 0; k0 < kKeys; k0 += 16) {
+        for (int k0 = 0; k0 < 32; k0 += 16) {
           uint32_t x[16], y[16];
-          tqtc::tmem_ld16(lane_base + 128 * s2 + k0, x);
-          if (SK) tqtc::tmem_ld16(lane_base + 128 * s2 + 64 + k0, y);
+          tqtc::tmem_ld16(s_col + 32 * half + k0, x);
+          if (SK) tqtc::tmem_ld16(s_col + 64 + 32 * half + k0, y);
           tqtc::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float v = SK ? fmaf(sm.b[s2][k0 + i], __uint_as_float(y[i]), sm.c[s2][k0 + i]) : sm.c[s2][k0 + i];
-            v = fmaf(sm.a[s2][k0 + i], __uint_as_float(x[i]), v) * rs;
-            t[k0 + i] = v;
-            mx = fmaxf(mx, v);
+          for (int i = 0; i < 16; i += 4) {
+            const ulonglong2 a2 = *reinterpret_cast<const ulonglong2*>(ka + k0 + i);
+            u64 u0 = mul2(a2.x, pair(x[i], x[i + 1])), u1 = mul2(a2.y, pair(x[i + 2], x[i + 3]));
+            if (SK) {
+              const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(kb + k0 + i);
+              u0 = fma2(b2.x, pair(y[i], y[i + 1]), u0);
+              u1 = fma2(b2.y, pair(y[i + 2], y[i + 3]), u1);
+            }
+            t[(k0 + i) / 2] = u0;
+            t[(k0 + i) / 2 + 1] = u1;
           }
         }
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        float z = 0.f;
-#pragma unroll
-        for (int k0 = 0; k0 < kKeys; k0 += 32) {
-          uint32_t hi[16], lo[16];
+        const int64_t left = (cur.seq < 0 ? A.Tp : sm.len[cur.seq]) - cur.t0 - 32 * half;  // keys of this half tile
+        if (left < 32) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float p0 = ex2(t[k0 + 2 * i] - ref), p1 = ex2(t[k0 + 2 * i + 1] - ref);
-            z += p0 + p1;
-            const float x = p0 * sm.v[s2][k0 + 2 * i], y = p1 * sm.v[s2][k0 + 2 * i + 1];
-            hi[i] = pack_f16(x, y);
+            const float2 f = parts(t[i]);
+            t[i] = pair(__float_as_uint(2 * i < left ? f.x : -INFINITY), __float_as_uint(2 * i + 1 < left ? f.y : -INFINITY));
+          }
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 f = parts(t[i]);
+          mx = fmaxf(mx, fmaxf(f.x, f.y));
+        }
+        sm.smax[turn & 1][half][r] = mx;
+        __syncwarp();
+        if (lane == 0) tqtc::mbar_arrive(&sm.pair[quad]);
+        WAIT_WARP(sm.pair[quad], turn & 1);
+        mx = fmaxf(M, fmaxf(mx, sm.smax[turn & 1][half ^ 1][r]) * rs);
+        ++turn;
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        const u64 rs2 = pair(rs), ref2 = pair(-ref);
+        u64 z = 0ull;
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const ulonglong2 v2 = *reinterpret_cast<const ulonglong2*>(kv + 2 * i);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const float2 e = parts(fma2(t[i + w], rs2, ref2));
+            const u64 p = pair(__float_as_uint(ex2(e.x)), __float_as_uint(ex2(e.y)));
+            z = add2(z, p);
+            const u64 pv = mul2(p, w ? v2.y : v2.x);
+            const float2 f = parts(pv);
+            hi[i + w] = pack_f16(f.x, f.y);
             if (SPLIT) {
-              const float2 f = unpack_f16(hi[i]);
-              lo[i] = pack_f16(x - f.x, y - f.y);
+              const float2 g = unpack_f16(hi[i + w]);
+              lo[i + w] = pack_f16(f.x - g.x, f.y - g.y);
             }
           }
-          tqtc::tmem_st16(lane_base + 128 * s2 + k0 / 2, hi);
-          if (SPLIT) tqtc::tmem_st16(lane_base + 128 * s2 + 32 + k0 / 2, lo);
         }
+        tqtc::tmem_st16(s_col + 16 * half, hi);
+        if (SPLIT) tqtc::tmem_st16(s_col + 32 + 16 * half, lo);
         tqtc::tmem_wait_st();
         if (act) {
-          Z = fmaf(Z, M == -INFINITY ? 0.f : ex2(M - ref), z);
+          const float2 f = parts(z);
+          Z = fmaf(Z, M == -INFINITY ? 0.f : ex2(M - ref), f.x + f.y);
           M = mx;
         }
       }
-      sm.mrow[j & 3][r] = M;
+      if (half == 0) sm.mrow[j & 3][r] = M;
       tqtc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        tqtc::mbar_arrive(&sm.sdone[s2]);
-        tqtc::mbar_arrive(&sm.pfull[s2]);
-      }
+      if (lane == 0) tqtc::mbar_arrive(&sm.pfull[s2]);
       cur.next(sm, A.Tp);
     }
-    if (mine) {
-      float* pr = A.partials + ((size_t)qrow * nC + c) * (D + 2);
-      pr[D] = M;
-      pr[D + 1] = Z;
-    }
-  } else if (warp < kExpWarp0) {
+    sm.zsum[half][r] = Z;
+  } else if (warp < kKeyWarp0) {
     // -------------------------------------------------------- accumulation
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegAcc));
     const int quad = warp & 3, half = (warp - kAccWarp0) >> 2;
     const int r = quad * 32 + lane;
     const bool mine = r < rows;
     const int myseq = mine ? r / A.G : -2;
     constexpr int NCOL = D / 2;
     const uint32_t o_base = tm + ((uint32_t)(quad * 32) << 16) + kColO + half * NCOL;
-    float acc[NCOL];
+    u64 acc[NCOL / 2];
 #pragma unroll
-    for (int i = 0; i < NCOL; ++i) acc[i] = 0.f;
+    for (int i = 0; i < NCOL / 2; ++i) acc[i] = 0ull;
     float M = -INFINITY;
     for (int j = 0; j < nt; ++j) {
       WAIT_WARP(sm.ofull, j & 1);
       tqtc::tc_fence_after();
       const bool act = mine && (cur.seq < 0 || cur.seq == myseq);
       if (__any_sync(TQ_FULL_MASK, act)) {
-        const float m2 = sm.mrow[j & 3][r], f = sm.f[j & 7];
-        const float al = act ? (m2 == M ? 1.f : ex2(M - m2)) : 1.f;
+        const float m2 = sm.mrow[j & 3][r];
+        const float al = act && m2 != M ? ex2(M - m2) : 1.f;
         if (__any_sync(TQ_FULL_MASK, al != 1.f)) {
+          const u64 a2 = pair(al);
 #pragma unroll
-          for (int i = 0; i < NCOL; ++i) acc[i] *= al;
+          for (int i = 0; i < NCOL / 2; ++i) acc[i] = mul2(acc[i], a2);
         }
         if (act) M = m2;
+        const u64 f2 = pair(sm.f[j & 7]);
 #pragma unroll
-        for (int k0 = 0; k0 < NCOL; k0 += 16) {
-          uint32_t x[16];
-          tqtc::tmem_ld16(o_base + k0, x);
+        for (int k0 = 0; k0 < NCOL; k0 += 8) {
+          uint32_t x[8];
+          tmem_ld8(o_base + k0, x);
           tqtc::tmem_wait_ld();
           if (act) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[k0 + i] = fmaf(__uint_as_float(x[i]), f, acc[k0 + i]);
+            for (int i = 0; i < 8; i += 2) acc[(k0 + i) / 2] = fma2(pair(x[i], x[i + 1]), f2, acc[(k0 + i) / 2]);
           }
         }
       }
@@ -461,180 +546,203 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* pr = A.partials + ((size_t)qrow * nC + c) * (D + 2);
       const float k = vp.inv_sqrt_d / kCenScale;
 #pragma unroll
-      for (int i = 0; i < NCOL; ++i) pr[coord_of(half * NCOL + i)] = acc[i] * k;
+      for (int i = 0; i < NCOL / 2; ++i) {
+        const float2 f = parts(acc[i]);
+        pr[coord_of(half * NCOL + 2 * i)] = f.x * k;
+        pr[coord_of(half * NCOL + 2 * i + 1)] = f.y * k;
+      }
+      if (half == 0) pr[D] = M;
     }
-  } else if (warp < kMmaWarp) {
-    // ----------------------------------------------------------- expansion
-    const int te = tid - kExpWarp0 * 32, key = te & 63, half = te >> 6;
-    const int ks = kp.nseg == 2 ? half : 0, vs = vp.nseg == 2 ? half : 0;
-    const int kw0 = kp.segbase[ks] + (kp.nseg == 2 ? 0 : half * NWH), vw0 = vp.segbase[vs] + (vp.nseg == 2 ? 0 : half * NWH);
-    const int kbits = kp.bits[ks], vbits = vp.bits[vs];
-    const Tab tk = sm.tab[0][ks], tv = sm.tab[1][vs];
+  } else if (warp < kValWarp0) {
+    // --------------------------------------------------- expansion of keys
+    const int te = tid - kKeyWarp0 * 32, key = te & 63, half = te >> 6;
+    const int ks = kp.nseg == 2 ? half : 0;
+    const int kw0 = kp.segbase[ks] + (kp.nseg == 2 ? 0 : half * NWH), kbits = kp.bits[ks];
+    const Tab tk = sm.tab[0][ks];
     const int off = (key >> 3) * 128 + (key & 7) * 16;
-    uint32_t kw[4][NWH], vw[4][NWH], sg[2];
+    uint32_t kw[4][NWH], sg[2] = {0u, 0u};
     float nu = 0.f, gam = 0.f, nv0 = 0.f, nv1 = 0.f;
-    bool kvalid = false;
-    auto load_k = [&](const Cursor& cu) {
+    auto load = [&](const Cursor& cu) {
       const bool pre = cu.seq < 0;
       const int64_t n = pre ? A.Tp : sm.len[cu.seq];
       const tq_compressed& K = pre ? A.Kp : A.K;
-      const tq_compressed& V = pre ? A.Vp : A.V;
-      const int64_t base = pre ? (int64_t)h * A.Tp : ((int64_t)(b0 + cu.seq) * A.Hkv + h) * A.T;
-      kvalid = cu.t0 + key < n;
-      const int64_t row = base + cu.t0 + key;
-      load_planes<NWH>(kw, K.codes + row * kp.W + kw0, kp.pw, kbits, kvalid);
+      const float* vn = pre ? A.Vp.norms : A.V.norms;
+      const int64_t first_row = (pre ? (int64_t)h * A.Tp : ((int64_t)(b0 + cu.seq) * A.Hkv + h) * A.T) + cu.t0;
+      const bool valid = cu.t0 + key < n;
+      const int64_t row = first_row + key;
+      load_planes<NWH>(kw, K.codes + row * kp.W + kw0, kp.pw, kbits, valid);
       if (SK) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) sg[i] = (kvalid && half + 2 * i < kp.MS) ? __ldg(K.signs + row * kp.MS + half + 2 * i) : 0u;
-        gam = kvalid ? __ldg(K.rnorms + row) : 0.f;
+        for (int i = 0; i < 2; ++i) sg[i] = (valid && half + 2 * i < kp.MS) ? __ldg(K.signs + row * kp.MS + half + 2 * i) : 0u;
+        gam = valid ? __ldg(K.rnorms + row) : 0.f;
       }
-      nu = kvalid ? __ldg(K.norms + row) : 0.f;
+      nu = valid ? __ldg(K.norms + row) : 0.f;
       // value norms of keys lane and lane + 32: every warp sees the whole tile
-      nv0 = cu.t0 + lane < n ? __ldg(V.norms + base + cu.t0 + lane) : 0.f;
-      nv1 = cu.t0 + 32 + lane < n ? __ldg(V.norms + base + cu.t0 + 32 + lane) : 0.f;
+      nv0 = cu.t0 + lane < n ? __ldg(vn + first_row + lane) : 0.f;
+      nv1 = cu.t0 + 32 + lane < n ? __ldg(vn + first_row + 32 + lane) : 0.f;
     };
-    auto load_v = [&](const Cursor& cu) {
-      const bool pre = cu.seq < 0;
-      const int64_t n = pre ? A.Tp : sm.len[cu.seq];
-      const int64_t base = pre ? (int64_t)h * A.Tp : ((int64_t)(b0 + cu.seq) * A.Hkv + h) * A.T;
-      const bool valid = cu.t0 + key < n;
-      load_planes<NWH>(vw, (pre ? A.Vp : A.V).codes + (base + cu.t0 + key) * vp.W + vw0, vp.pw, vbits, valid);
-    };
-    Cursor ck = cur, cv = cur;
-    if (nt > 0) {
-      load_k(ck);
-      load_v(cv);
-    }
+    if (nt > 0) load(cur);
     const float ca = A.scale_log2e * kp.inv_sqrt_d / kCenScale, cb = A.scale_log2e * kp.qjl_coef;
-    // keys of tile j, then the values of tile j - 1
-    for (int j = 0; j <= nt; ++j) {
-      if (j < nt) {
-        const int s2 = j & 1;
-        if (j >= 2) {
-          WAIT_WARP(sm.kempty[s2], ((j >> 1) & 1) ^ 1);
-          WAIT_WARP(sm.sdone[s2], ((j >> 1) & 1) ^ 1);
-        }
-        unsigned char* st = dyn + lay.k + s2 * lay.kstage;
+    for (int j = 0; j < nt; ++j) {
+      const int s2 = j & 1;
+      // QK(j - 2) done also means that softmax(j - 4) is: its product with the
+      // values was issued before, so the scalars' slot j & 3 is free
+      if (j >= 2) WAIT_WARP(sm.kempty[s2], ((j >> 1) & 1) ^ 1);
+      unsigned char* st = dyn + lay.k + s2 * lay.kstage;
 #pragma unroll
-        for (int i = 0; i < NWH; ++i) {
-          const uint32_t pl[4] = {kw[0][i], kw[1][i], kw[2][i], kw[3][i]};
-          expand_group<SPLIT>(kbits, pl, tk, st + (half * NWH + i) * 4096 + off, L::kpart);
-        }
-        if (SK) {
+      for (int i = 0; i < NWH; ++i) {
+        const uint32_t pl[4] = {kw[0][i], kw[1][i], kw[2][i], kw[3][i]};
+        expand_group<SPLIT>(kbits, pl, tk, st + (half * NWH + i) * 4096 + off, L::kpart);
+      }
+      if (SK) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int w = half + 2 * i;
-            if (w < kp.MS) {
+        for (int i = 0; i < 2; ++i) {
+          const int w = half + 2 * i;
+          if (w < kp.MS) {
 #pragma unroll
-              for (int ch = 0; ch < 4; ++ch) {
-                uint4 x;
-                x.x = ((sg[i] << (15 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
-                x.y = ((sg[i] << (14 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
-                x.z = ((sg[i] << (13 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
-                x.w = ((sg[i] << (12 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
-                *reinterpret_cast<uint4*>(st + lay.sg + (4 * w + ch) * 1024 + off) = x;
-              }
+            for (int ch = 0; ch < 4; ++ch) {
+              uint4 x;
+              x.x = ((sg[i] << (15 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
+              x.y = ((sg[i] << (14 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
+              x.z = ((sg[i] << (13 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
+              x.w = ((sg[i] << (12 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
+              *reinterpret_cast<uint4*>(st + lay.sg + (4 * w + ch) * 1024 + off) = x;
             }
           }
         }
-        float nm = fmaxf(fabsf(nv0), fabsf(nv1));
-        nm = tq_warp_max(nm);
-        int e = 0;
-        if (nm > 0.f && nm < INFINITY) e = max(-100, ilogbf(nm) + 1);
-        const float dn = ldexpf(1.f, 14 - e);
-        if (half == 0) {
-          sm.a[s2][key] = nu * ca;
-          sm.b[s2][key] = nu * gam * cb;
-          sm.c[s2][key] = kvalid ? 0.f : -INFINITY;
-          sm.v[s2][key] = ((key & 32) ? nv1 : nv0) * dn;
-          if (key == 0) sm.f[j & 7] = ldexpf(1.f, e - 14);
-        }
-        tqtc::fence_proxy_async_smem();
-        tqtc::mbar_arrive(&sm.kfull[s2]);
-        if (j + 1 < nt) {
-          ck.next(sm, A.Tp);
-          load_k(ck);
-        }
       }
-      if (j > 0) {
-        const int i0 = j - 1, sv = L::VST == 2 ? (i0 & 1) : 0, use = L::VST == 2 ? (i0 >> 1) : i0;
-        if (use >= 1) WAIT_WARP(sm.vempty[sv], (use & 1) ^ 1);
-        unsigned char* st = dyn + lay.v + sv * L::NP * L::kpart;
-#pragma unroll
-        for (int i = 0; i < NWH; ++i) {
-          const uint32_t pl[4] = {vw[0][i], vw[1][i], vw[2][i], vw[3][i]};
-          expand_group<SPLIT>(vbits, pl, tv, st + (half * NWH + i) * 4096 + off, L::kpart);
-        }
-        tqtc::fence_proxy_async_smem();
-        tqtc::mbar_arrive(&sm.vfull[sv]);
-        if (j < nt) {
-          cv.next(sm, A.Tp);
-          load_v(cv);
-        }
+      if (half == 0) {
+        const float nm = tq_warp_max(fmaxf(fabsf(nv0), fabsf(nv1)));
+        const int e = max(-100, exponent_of(nm) + 1);  // |nv| < 2^e
+        sm.a[j & 3][key] = nu * ca;
+        sm.b[j & 3][key] = nu * gam * cb;
+        sm.v[j & 3][key] = ((key & 32) ? nv1 : nv0) * pow2(14 - e);
+        if (key == 0) sm.f[j & 7] = pow2(e - 14);
+      }
+      tqtc::fence_proxy_async_smem();
+      tqtc::mbar_arrive(&sm.kfull[s2]);
+      if (j + 1 < nt) {
+        cur.next(sm, A.Tp);
+        load(cur);
       }
     }
-  } else if (lane == 0 && nt > 0) {
+  } else if (warp < kMmaWarp) {
+    // ------------------------------------------------- expansion of values
+    const int te = tid - kValWarp0 * 32, key = te & 63, half = te >> 6;
+    const int vs = vp.nseg == 2 ? half : 0;
+    const int vw0 = vp.segbase[vs] + (vp.nseg == 2 ? 0 : half * NWH), vbits = vp.bits[vs];
+    const Tab tv = sm.tab[1][vs];
+    const int off = (key >> 3) * 128 + (key & 7) * 16;
+    uint32_t vw[4][NWH];
+    auto load = [&](const Cursor& cu) {
+      const bool pre = cu.seq < 0;
+      const int64_t n = pre ? A.Tp : sm.len[cu.seq];
+      const int64_t base = pre ? (int64_t)h * A.Tp : ((int64_t)(b0 + cu.seq) * A.Hkv + h) * A.T;
+      load_planes<NWH>(vw, (pre ? A.Vp : A.V).codes + (base + cu.t0 + key) * vp.W + vw0, vp.pw, vbits, cu.t0 + key < n);
+    };
+    if (nt > 0) load(cur);
+    for (int j = 0; j < nt; ++j) {
+      const int sv = L::VST == 2 ? (j & 1) : 0, use = L::VST == 2 ? (j >> 1) : j;
+      if (use >= 1) WAIT_WARP(sm.vempty[sv], (use & 1) ^ 1);
+      unsigned char* st = dyn + lay.v + sv * L::NP * L::kpart;
+#pragma unroll
+      for (int i = 0; i < NWH; ++i) {
+        const uint32_t pl[4] = {vw[0][i], vw[1][i], vw[2][i], vw[3][i]};
+        expand_group<SPLIT>(vbits, pl, tv, st + (half * NWH + i) * 4096 + off, L::kpart);
+      }
+      tqtc::fence_proxy_async_smem();
+      tqtc::mbar_arrive(&sm.vfull[sv]);
+      if (j + 1 < nt) {
+        cur.next(sm, A.Tp);
+        load(cur);
+      }
+    }
+  } else {
     // ----------------------------------------------------------- MMA issue
-    constexpr uint32_t idS = tqtc::instr_desc(1, 0, 0, 128, kKeys);
-    constexpr uint32_t idO = tqtc::instr_desc(1, 0, 0, 128, D) | (1u << 16);  // B with its N index contiguous
-    const uint32_t base = tqtc::smem_u32(dyn);
-    for (int j = 0; j <= nt; ++j) {
-      if (j < nt) {
-        const int s2 = j & 1, ph = (j >> 1) & 1;
-        if (j == 0) WAIT_ONE(sm.qfull, 0);
-        WAIT_ONE(sm.kfull[s2], ph);
-        tqtc::tc_fence_after();
-        const uint32_t dS = tm + 128 * s2, kst = base + lay.k + s2 * lay.kstage;
-        // parts: low queries, low keys, then the high product
+    // The whole warp walks the loop with warp-uniform values and one elected
+    // lane issues: an issue loop inside a single-lane branch costs 48 cycles
+    // per 32-cycle product (measured), this one 33.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegMma));
+    if (__shfl_sync(TQ_FULL_MASK, warp, 0) == kMmaWarp && nt > 0) {
+      constexpr uint32_t idS = tqtc::instr_desc(1, 0, 0, 128, kKeys);
+      constexpr uint32_t idO = tqtc::instr_desc(1, 0, 0, 128, D) | (1u << 16);  // B with its N index contiguous
+      const uint32_t base = __shfl_sync(TQ_FULL_MASK, tqtc::smem_u32(dyn), 0);
+      const uint32_t tu = __shfl_sync(TQ_FULL_MASK, tm, 0);
+      const int ks = kp.m / 32;
+      for (int j = 0; j <= nt; ++j) {
+        if (j < nt) {
+          const int s2 = j & 1, ph = (j >> 1) & 1;
+          if (j == 0) WAIT_WARP(sm.qfull, 0);
+          WAIT_WARP(sm.kfull[s2], ph);
+          tqtc::tc_fence_after();
+          if (elect()) {
+            const uint32_t dS = tu + 128 * s2, kst = base + lay.k + s2 * lay.kstage;
+            // parts: low queries, low keys, then the high product
 #pragma unroll
-        for (int pr = SPLIT ? 0 : 2; pr < 3; ++pr) {
-          const uint32_t qa = tm + kColQ + (pr == 0 ? D / 2 : 0), kb = kst + (pr == 1 ? L::kpart : 0);
+            for (int pr = SPLIT ? 0 : 2; pr < 3; ++pr) {
+              const uint32_t qa = tu + kColQ + (pr == 0 ? D / 2 : 0);
+              const uint64_t kd = tqtc::smem_desc(kst + (pr == 1 ? L::kpart : 0), 1024, 128);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tqtc::mma_f16_ts(dS, qa + 8 * k, tqtc::smem_desc(kb + 2048 * k, 1024, 128), idS,
-                             !(k == 0 && pr == (SPLIT ? 0 : 2)));
-        }
-        if (SK) {
-          for (int pr = SPLIT ? 0 : 1; pr < 2; ++pr) {
-            const uint32_t wa = base + lay.w + (pr == 0 ? kRows * kp.m * 2 : 0);
-            for (int k = 0; k < kp.m / 16; ++k)
-              tqtc::mma_f16_ss(dS + 64, tqtc::smem_desc(wa + 4096 * k, 2048, 128),
-                               tqtc::smem_desc(kst + lay.sg + 2048 * k, 1024, 128), idS,
-                               !(k == 0 && pr == (SPLIT ? 0 : 1)));
+              for (int k = 0; k < D / 16; ++k)
+                tqtc::mma_f16_ts(dS, qa + 8 * k, kd + 128 * k, idS, !(k == 0 && pr == (SPLIT ? 0 : 2)));
+            }
+            if (SK) {
+              const uint64_t sd = tqtc::smem_desc(kst + lay.sg, 1024, 128);
+#pragma unroll
+              for (int pr = SPLIT ? 0 : 1; pr < 2; ++pr) {
+                const uint64_t wd = tqtc::smem_desc(base + lay.w + (pr == 0 ? kRows * kp.m * 2 : 0), 2048, 128);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (k < ks) {
+                    tqtc::mma_f16_ss(dS + 64, wd + 512 * k, sd + 256 * k, idS, !(k == 0 && pr == (SPLIT ? 0 : 1)));
+                    tqtc::mma_f16_ss(dS + 64, wd + 512 * k + 256, sd + 256 * k + 128, idS, true);
+                  }
+                }
+              }
+            }
+            tqtc::mma_commit(&sm.kempty[s2]);
+            tqtc::mma_commit(&sm.sfull[s2]);
           }
+          __syncwarp();
         }
-        tqtc::mma_commit(&sm.kempty[s2]);
-        tqtc::mma_commit(&sm.sfull[s2]);
-      }
-      if (j > 0) {
-        const int i0 = j - 1, s2 = i0 & 1, ph = (i0 >> 1) & 1;
-        const int sv = L::VST == 2 ? s2 : 0, use = L::VST == 2 ? (i0 >> 1) : i0;
-        WAIT_ONE(sm.pfull[s2], ph);
-        WAIT_ONE(sm.vfull[sv], use & 1);
-        if (i0 >= 1) WAIT_ONE(sm.oempty, (i0 & 1) ^ 1);
-        tqtc::tc_fence_after();
-        const uint32_t dO = tm + kColO, pA = tm + 128 * s2, vst = base + lay.v + sv * L::NP * L::kpart;
+        if (j > 0) {
+          const int i0 = j - 1, s2 = i0 & 1, ph = (i0 >> 1) & 1;
+          const int sv = L::VST == 2 ? s2 : 0, use = L::VST == 2 ? (i0 >> 1) : i0;
+          WAIT_WARP(sm.pfull[s2], ph);
+          WAIT_WARP(sm.vfull[sv], use & 1);
+          if (i0 >= 1) WAIT_WARP(sm.oempty, (i0 & 1) ^ 1);
+          tqtc::tc_fence_after();
+          if (elect()) {
+            const uint32_t dO = tu + kColO, pA = tu + 128 * s2, vst = base + lay.v + sv * L::NP * L::kpart;
 #pragma unroll
-        for (int pr = SPLIT ? 0 : 2; pr < 3; ++pr) {
-          const uint32_t pa = pA + (pr == 0 ? 32 : 0), vb = vst + (pr == 1 ? L::kpart : 0);
+            for (int pr = SPLIT ? 0 : 2; pr < 3; ++pr) {
+              const uint32_t pa = pA + (pr == 0 ? 32 : 0);
+              const uint64_t vd = tqtc::smem_desc(vst + (pr == 1 ? L::kpart : 0), 128, 1024);
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            tqtc::mma_f16_ts(dO, pa + 8 * k, tqtc::smem_desc(vb + 256 * k, 128, 1024), idO,
-                             !(k == 0 && pr == (SPLIT ? 0 : 2)));
+              for (int k = 0; k < kKeys / 16; ++k)
+                tqtc::mma_f16_ts(dO, pa + 8 * k, vd + 16 * k, idO, !(k == 0 && pr == (SPLIT ? 0 : 2)));
+            }
+            tqtc::mma_commit(&sm.vempty[sv]);
+            tqtc::mma_commit(&sm.ofull);
+          }
+          __syncwarp();
         }
-        tqtc::mma_commit(&sm.vempty[sv]);
-        tqtc::mma_commit(&sm.ofull);
       }
+      // every product and commit has landed before the block ends
+      if (elect()) tqtc::mma_commit(&sm.done);
+      __syncwarp();
+      if (!tqtc::mbar_wait(&sm.done, 0)) fail();
     }
-    // every product and commit has landed before the block ends
-    tqtc::mma_commit(&sm.done);
-    if (!tqtc::mbar_wait(&sm.done, 0)) fail();
   }
 #undef WAIT_WARP
-#undef WAIT_ONE
   __syncwarp();
   tqtc::tc_fence_before();
   __syncthreads();
+  if (tid < rows) {
+    // the two halves' sums (their exponentials refer to the same maxima)
+    const int qrow = (b0 + tid / A.G) * A.Hq + h * A.G + tid % A.G;
+    A.partials[((size_t)qrow * nC + c) * (D + 2) + D + 1] = sm.zsum[0][tid] + sm.zsum[1][tid];
+  }
   if (warp == kMmaWarp) {
     tqtc::tc_fence_after();
     tqtc::tmem_dealloc(tm, 512);
