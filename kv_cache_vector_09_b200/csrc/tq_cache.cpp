@@ -100,10 +100,17 @@ tq_prefix_plan plan_of(const tq_params& kp, const tq_params& vp, int B, int Hq, 
   return pl;
 }
 
-size_t qprep_size(const tq_params& p, int64_t rows) { return align256(sizeof(float) * (size_t)rows * (p.d + p.m)); }
+// the prepared queries, then the partials
+size_t query_bytes(const tq_params& kp, int B, int Hq, int Hkv, const tq_prefix_plan& pl, size_t* scales_at) {
+  *scales_at = 0;
+  if (pl.tc) return align256(tq_prefix_tc_bytes(kp, B, Hkv, Hq / Hkv, scales_at));
+  return align256(sizeof(float) * (size_t)B * Hq * (kp.d + kp.m));
+}
 
-size_t prefix_bytes(const tq_params& kp, const tq_params& vp, int64_t rows, const tq_prefix_plan& pl) {
-  return qprep_size(kp, rows) + align256(sizeof(float) * (size_t)rows * (pl.nP + pl.nO) * (size_t)(vp.d + 2 + vp.m));
+size_t prefix_bytes(const tq_params& kp, const tq_params& vp, int B, int Hq, int Hkv, const tq_prefix_plan& pl) {
+  size_t at;
+  return query_bytes(kp, B, Hq, Hkv, pl, &at) +
+         align256(sizeof(float) * (size_t)B * Hq * (pl.nP + pl.nO) * (size_t)(vp.d + 2 + vp.m));
 }
 
 tq_status prefix_shape(const tq_codec* kc, const tq_codec* vc, int B, int Hq, int Hkv, int64_t Tp, int64_t T,
@@ -127,7 +134,7 @@ extern "C" tq_status tq_attend_prefix_workspace_size(const tq_codec* kc, const t
   tq_status st = prefix_shape(kc, vc, B, Hq, Hkv, Tp, T, name);
   if (st != TQ_OK) return st;
   const tq_prefix_plan pl = plan_of(kc->p, vc->p, B, Hq, Hkv, Tp, T, sms_of(kc->device < 0 ? 0 : kc->device));
-  *bytes = prefix_bytes(kc->p, vc->p, (int64_t)B * Hq, pl);
+  *bytes = prefix_bytes(kc->p, vc->p, B, Hq, Hkv, pl);
   return TQ_OK;
 }
 
@@ -154,8 +161,7 @@ extern "C" tq_status tq_attend_prefix(const tq_codec* kc, const tq_codec* vc, co
   if (T > 0 && ((st = rows_ok(kc, K, name, "K")) != TQ_OK || (st = rows_ok(vc, V, name, "V")) != TQ_OK)) return st;
   tq_prefix_plan pl = plan_of(kc->p, vc->p, B, Hq, Hkv, Tp, T, sms_of(kc->device));
   pl.split = out_dtype != TQ_BF16 || lse != nullptr;
-  const int64_t rows = (int64_t)B * Hq;
-  const size_t need = prefix_bytes(kc->p, vc->p, rows, pl);
+  const size_t need = prefix_bytes(kc->p, vc->p, B, Hq, Hkv, pl);
   if (!aligned(workspace, 16) || ws_bytes < need)
     return tq_fail(TQ_ERR_INVALID_ARG, "%s: workspace null, misaligned or smaller than %zu bytes", name, need);
   const cudaStream_t s = (cudaStream_t)stream;
@@ -170,11 +176,20 @@ extern "C" tq_status tq_attend_prefix(const tq_codec* kc, const tq_codec* vc, co
   if (Tp > 0) a.Kp = *Kp, a.Vp = *Vp;
   if (T > 0) a.K = *K, a.V = *V;
   a.scale_log2e = (scale == 0.0f ? kc->p.inv_sqrt_d : scale) * 1.4426950408889634f;
-  a.qprep = (const float*)workspace;
-  a.partials = (float*)((char*)workspace + qprep_size(kc->p, rows));
-  cudaError_t e = tq_launch_qprep(kc->p, q, dt, (int)rows, (float*)workspace, s);
-  if (e == cudaSuccess && pl.nP + pl.nO > 0)
-    e = pl.tc ? tq_launch_prefix_tc(kc->p, vc->p, a, pl, s) : tq_launch_prefix_any(kc->p, vc->p, a, pl, s);
+  size_t scales_at;
+  a.q = q;
+  a.dtype = dt;
+  a.partials = (float*)((char*)workspace + query_bytes(kc->p, B, Hq, Hkv, pl, &scales_at));
+  cudaError_t e = cudaSuccess;
+  if (pl.nP + pl.nO > 0 && pl.tc) {
+    a.image = (unsigned char*)workspace;
+    a.scales = (float*)((char*)workspace + scales_at);
+    e = tq_launch_prefix_tc(kc->p, vc->p, a, pl, s);
+  } else if (pl.nP + pl.nO > 0) {
+    a.qprep = (const float*)workspace;
+    e = tq_launch_qprep(kc->p, q, dt, B * Hq, (float*)workspace, s);
+    if (e == cudaSuccess) e = tq_launch_prefix_any(kc->p, vc->p, a, pl, s);
+  }
   if (e == cudaSuccess) e = tq_launch_prefix_combine(vc->p, a, pl, out, out_dtype, lse, s);
   return done(e, name);
 }

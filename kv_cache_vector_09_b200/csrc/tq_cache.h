@@ -24,14 +24,19 @@ struct tq_prefix_args {
   const int32_t* lens;  // [B] or null (all T)
   tq_compressed Kp, Vp, K, V;
   float scale_log2e;
-  const float* qprep;  // [B * Hq][d + m]
+  const void* q;        // [B][Hq][d]
+  tq_dtype dtype;
+  const float* qprep;   // [B * Hq][d + m] (CUDA-core kernel)
+  unsigned char* image; // query images and row scales (tensor-core kernel)
+  float* scales;
   float* partials;     // [B * Hq][nP + nO][d + 2 + m_v]
 };
 
 cudaError_t tq_launch_prefix_any(const tq_params& kp, const tq_params& vp, const tq_prefix_args& a,
                                  const tq_prefix_plan& plan, cudaStream_t st);
-// whether the codecs have the tensor-core kernel, and its launch
+// whether the codecs have the tensor-core kernel, its query images' bytes, and its launch
 bool tq_prefix_tc_supported(const tq_params& kp, const tq_params& vp);
+size_t tq_prefix_tc_bytes(const tq_params& kp, int B, int Hkv, int G, size_t* scales_at);
 cudaError_t tq_launch_prefix_tc(const tq_params& kp, const tq_params& vp, const tq_prefix_args& a,
                                 const tq_prefix_plan& plan, cudaStream_t st);
 cudaError_t tq_launch_prefix_combine(const tq_params& vp, const tq_prefix_args& a, const tq_prefix_plan& plan,

@@ -254,6 +254,117 @@ struct Cursor {
   }
 };
 
+// Query image of one group (KV head h, row block rb): for each of its kRows rows
+// the fp16 parts of up * q' and of up * S q' in the order of the key operands,
+//   [part][position / 8][row][8], positions [0, D) of q', then [0, m) of S q',
+// and 1 / up, the power of two that brings the row's largest element to
+// [2^9, 2^10).  Rows behind the last query are zero.
+template <int D>
+__host__ __device__ inline size_t image_part_bytes(int m) {
+  return (size_t)kRows * (D + m) * 2;
+}
+
+// One block: 16 rows of one group.  Two warps of eight rotate a row pair each
+// (Hadamard, or the dense Haar rotation), then thread (c, half) sums sketch row
+// c for eight rows from the transposed sketch, whose columns are coalesced:
+// the sketch is read once for 16 queries instead of once a query.
+constexpr int kPrepRows = 16;
+
+template <int D, typename TIn>
+__global__ void __launch_bounds__(256)
+    prefix_prep_kernel(const tq_params p, const TIn* __restrict__ q, const int B, const int Hq, const int G,
+                       const int SB, unsigned char* __restrict__ img, float* __restrict__ scales) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int VPL = D / 32;
+  __shared__ __align__(16) float qt[D][kPrepRows];  // q' transposed
+  __shared__ float wt[128][kPrepRows + 1];          // S q' transposed
+  __shared__ float buf[8][D], s_up[kPrepRows];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nrb = (B + SB - 1) / SB;
+  const int part = blockIdx.x % (kRows / kPrepRows), grp = blockIdx.x / (kRows / kPrepRows);
+  const int rb = grp % nrb, h = grp / nrb, m = p.m;
+  const int b0 = rb * SB, rows = min(SB, B - b0) * G, r0 = part * kPrepRows;
+  for (int i = warp; i < kPrepRows; i += 8) {
+    const int r = r0 + i;
+    float v[VPL];
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) v[k] = 0.f;
+    if (r < rows) {
+      const TIn* src = q + (size_t)((b0 + r / G) * Hq + h * G + r % G) * D;
+#pragma unroll
+      for (int k = 0; k < VPL; ++k) {
+        const float x = tq_to_f32(src[lane + 32 * k]);
+        v[k] = tq_dneg(p.dbits, k, lane) ? -x : x;
+      }
+      if (p.haar) {
+        tq_dense_rotate_warp<VPL>(v, lane, p.piT, buf[warp]);
+      } else {
+        tq_fwht_warp<VPL>(v, lane);
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) v[k] *= p.inv_sqrt_p;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) qt[lane + 32 * k][i] = v[k];
+  }
+  __syncthreads();
+  for (int u = tid; u < 2 * m; u += 256) {
+    const int c = u % m, half = u / m, Q = m / 32;
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+#pragma unroll 16
+    for (int i = 0; i < D; ++i) {
+      const float s = __ldg(p.St + (size_t)i * m + c);
+      const float4 x = *reinterpret_cast<const float4*>(&qt[i][8 * half]);
+      const float4 y = *reinterpret_cast<const float4*>(&qt[i][8 * half + 4]);
+      acc[0] = fmaf(s, x.x, acc[0]);
+      acc[1] = fmaf(s, x.y, acc[1]);
+      acc[2] = fmaf(s, x.z, acc[2]);
+      acc[3] = fmaf(s, x.w, acc[3]);
+      acc[4] = fmaf(s, y.x, acc[4]);
+      acc[5] = fmaf(s, y.y, acc[5]);
+      acc[6] = fmaf(s, y.z, acc[6]);
+      acc[7] = fmaf(s, y.w, acc[7]);
+    }
+    const int j = c / Q + 32 * (c % Q);  // St's column c is sketch row j
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wt[j][8 * half + i] = acc[i];
+  }
+  __syncthreads();
+  for (int i = warp; i < kPrepRows; i += 8) {
+    float mx = 0.f;
+    for (int k = lane; k < D; k += 32) mx = fmaxf(mx, fabsf(qt[k][i]));
+    for (int k = lane; k < m; k += 32) mx = fmaxf(mx, fabsf(wt[k][i]));
+    mx = tq_warp_max(mx);
+    const int ex = mx > 0.f && mx < INFINITY ? max(-100, min(100, exponent_of(mx))) : 9;
+    if (lane == 0) {
+      s_up[i] = pow2(9 - ex);
+      scales[(size_t)grp * kRows + r0 + i] = pow2(ex - 9);
+    }
+  }
+  __syncthreads();
+  unsigned char* out = img + (size_t)grp * 2 * image_part_bytes<D>(m);
+  for (int u = tid; u < (D + m) / 8 * kPrepRows; u += 256) {
+    const int i = u % kPrepRows, ch = u / kPrepRows;
+    uint4 hi, lo;
+    uint32_t* ph = reinterpret_cast<uint32_t*>(&hi);
+    uint32_t* pl = reinterpret_cast<uint32_t*>(&lo);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int p0 = 8 * ch + 2 * k - (8 * ch < D ? 0 : D);
+      const float x = (8 * ch < D ? qt[coord_of(p0)][i] : wt[sketch_of(p0)][i]) * s_up[i];
+      const float y = (8 * ch < D ? qt[coord_of(p0 + 1)][i] : wt[sketch_of(p0 + 1)][i]) * s_up[i];
+      ph[k] = pack_f16(x, y);
+      const float2 f = unpack_f16(ph[k]);
+      pl[k] = pack_f16(x - f.x, y - f.y);
+    }
+    const size_t at = ((size_t)ch * kRows + r0 + i) * 16;
+    *reinterpret_cast<uint4*>(out + at) = hi;
+    *reinterpret_cast<uint4*>(out + image_part_bytes<D>(m) + at) = lo;
+  }
+}
+
 template <int D, bool SPLIT, bool SK>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const tq_params kp, const tq_params vp, const tq_prefix_args A, const int nC, const int SB) {
@@ -345,65 +456,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, half = warp >> 2, r = quad * 32 + lane;
     const uint32_t lane_base = tm + ((uint32_t)(quad * 32) << 16);
     const bool mine = r < rows;
-    const int qrow = mine ? (b0 + r / A.G) * A.Hq + h * A.G + r % A.G : 0;
     const int myseq = mine ? r / A.G : -2;
-    const float* q = A.qprep + (size_t)qrow * (D + kp.m);
     float rs = 1.f, M = -INFINITY, Z = 0.f;
     int turn = 0;  // phases of this quadrant's pair of warps
-    for (int once = 0; once < 1 && nt > 0; ++once) {
-      // the row's power-of-two scale: its largest element to [2^9, 2^10)
+    // the query image is the preceding launch's; every block waits for it, so
+    // that this kernel never ends before that one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (nt > 0) {
+      const size_t grp = (size_t)h * nrb + rb;
+      const unsigned char* img = A.image + grp * 2 * image_part_bytes<D>(kp.m);
+      rs = A.scales[grp * kRows + r];
+      // q' to TMEM: this half its share of the columns; S q' to shared memory
       if (quad * 32 < rows) {
-        float mx = 0.f;
-        if (mine)
-          for (int i = half ? D : 0; i < (half ? D + kp.m : D); i += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(q + i);
-            mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
-          }
-        sm.smax[turn & 1][half][r] = mx;
-        __syncwarp();
-        if (lane == 0) tqtc::mbar_arrive(&sm.pair[quad]);
-        WAIT_WARP(sm.pair[quad], turn & 1);
-        mx = fmaxf(mx, sm.smax[turn & 1][half ^ 1][r]);
-        ++turn;
-        float up = 1.f;
-        if (mx > 0.f && mx < INFINITY) {
-          const int ex = max(-100, min(100, exponent_of(mx)));
-          up = pow2(9 - ex);
-          rs = pow2(ex - 9);
-        }
-        if (half == 0) {
-#pragma unroll 1
-          for (int g = 0; g < D / 32; ++g) {
-            uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float x = mine ? q[coord_of(32 * g + 2 * i)] * up : 0.f, y = mine ? q[coord_of(32 * g + 2 * i + 1)] * up : 0.f;
-              hi[i] = pack_f16(x, y);
-              const float2 f = unpack_f16(hi[i]);
-              lo[i] = pack_f16(x - f.x, y - f.y);
-            }
-            tqtc::tmem_st16(lane_base + kColQ + 16 * g, hi);
-            if (SPLIT) tqtc::tmem_st16(lane_base + kColQ + D / 2 + 16 * g, lo);
-          }
-          tqtc::tmem_wait_st();
-        } else if (SK) {
-          const float* w = q + D;
-#pragma unroll 1
-          for (int ch = 0; ch < kp.m / 8; ++ch) {
-            uint4 hi, lo;
-            uint32_t* ph = reinterpret_cast<uint32_t*>(&hi);
-            uint32_t* pl = reinterpret_cast<uint32_t*>(&lo);
+        for (int part = 0; part < L::NP; ++part) {
+#pragma unroll
+          for (int g = 0; g < D / 64; ++g) {
+            uint32_t x[16];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float x = mine ? w[sketch_of(8 * ch + 2 * i)] * up : 0.f, y = mine ? w[sketch_of(8 * ch + 2 * i + 1)] * up : 0.f;
-              ph[i] = pack_f16(x, y);
-              const float2 f = unpack_f16(ph[i]);
-              pl[i] = pack_f16(x - f.x, y - f.y);
+              const uint4 v = *reinterpret_cast<const uint4*>(img + part * image_part_bytes<D>(kp.m) +
+                                                              ((size_t)(4 * (half * (D / 64) + g) + i) * kRows + r) * 16);
+              x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
             }
-            unsigned char* dst = dyn + lay.w + ch * 2048 + (r >> 3) * 128 + (r & 7) * 16;
-            *reinterpret_cast<uint4*>(dst) = hi;
-            if (SPLIT) *reinterpret_cast<uint4*>(dst + kRows * kp.m * 2) = lo;
+            tqtc::tmem_st16(lane_base + kColQ + part * (D / 2) + 16 * (half * (D / 64) + g), x);
           }
+        }
+        tqtc::tmem_wait_st();
+        if (SK) {
+#pragma unroll
+          for (int part = 0; part < L::NP; ++part)
+#pragma unroll 4
+            for (int ch = half; ch < kp.m / 8; ch += 2)
+              *reinterpret_cast<uint4*>(dyn + lay.w + part * kRows * kp.m * 2 + ch * 2048 + r * 16) =
+                  *reinterpret_cast<const uint4*>(img + part * image_part_bytes<D>(kp.m) + ((size_t)(D / 8 + ch) * kRows + r) * 16);
           tqtc::fence_proxy_async_smem();
         }
       }
@@ -750,14 +836,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool SPLIT, bool SK>
-cudaError_t launch(const tq_params& kp, const tq_params& vp, const tq_prefix_args& a, int nC, int SB, unsigned grid,
+cudaError_t launch(const tq_params& kp, const tq_params& vp, const tq_prefix_args& a, int nC, int SB, unsigned groups,
                    cudaStream_t st) {
   const Layout<D, SPLIT> lay(kp.m);
   auto fn = prefix_tc_kernel<D, SPLIT, SK>;
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, lay.total);
   if (e != cudaSuccess) return e;
-  fn<<<grid, kThreads, lay.total, st>>>(kp, vp, a, nC, SB);
-  return cudaGetLastError();
+  const dim3 prep(groups * (kRows / kPrepRows));
+  unsigned char* img = a.image;
+  float* sc = a.scales;
+  switch (a.dtype) {
+    case TQ_F32: prefix_prep_kernel<D, float><<<prep, 256, 0, st>>>(kp, (const float*)a.q, a.B, a.Hq, a.G, SB, img, sc); break;
+    case TQ_BF16:
+      prefix_prep_kernel<D, __nv_bfloat16><<<prep, 256, 0, st>>>(kp, (const __nv_bfloat16*)a.q, a.B, a.Hq, a.G, SB, img, sc);
+      break;
+    default: prefix_prep_kernel<D, __half><<<prep, 256, 0, st>>>(kp, (const __half*)a.q, a.B, a.Hq, a.G, SB, img, sc);
+  }
+  // programmatic dependent launch: the blocks set up and expand their first
+  // tiles while the queries are prepared, and wait for the image where they read it
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(groups * nC);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = lay.total;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, kp, vp, a, nC, SB);
 }
 
 }  // namespace
@@ -766,12 +873,21 @@ bool tq_prefix_tc_supported(const tq_params& kp, const tq_params& vp) {
   return (kp.d == 64 || kp.d == 128) && kp.m <= 128 && vp.m == 0 && !kp.vq_bits && !vp.vq_bits;
 }
 
+static int64_t groups_of(int B, int Hkv, int G) { return (int64_t)Hkv * ((B + kRows / G - 1) / (kRows / G)); }
+
+// query images (two fp16 parts), then the rows' scales
+size_t tq_prefix_tc_bytes(const tq_params& kp, int B, int Hkv, int G, size_t* scales_at) {
+  const size_t groups = (size_t)groups_of(B, Hkv, G);
+  *scales_at = groups * 2 * kRows * (size_t)(kp.d + kp.m) * 2;
+  return *scales_at + groups * kRows * sizeof(float);
+}
+
 cudaError_t tq_launch_prefix_tc(const tq_params& kp, const tq_params& vp, const tq_prefix_args& a,
                                 const tq_prefix_plan& plan, cudaStream_t st) {
   const int SB = kRows / a.G;
-  const int64_t grid = (int64_t)a.Hkv * ((a.B + SB - 1) / SB) * plan.nP;
-  if (grid > 0x7fffffffll) return cudaErrorNotSupported;
-  const unsigned g = (unsigned)grid;
+  const int64_t groups = groups_of(a.B, a.Hkv, a.G);
+  if (groups * std::max(plan.nP, kRows / kPrepRows) > 0x7fffffffll) return cudaErrorNotSupported;
+  const unsigned g = (unsigned)groups;
 #define GO(DD, SS) \
   return kp.m ? launch<DD, SS, true>(kp, vp, a, plan.nP, SB, g, st) : launch<DD, SS, false>(kp, vp, a, plan.nP, SB, g, st)
   if (kp.d == 64) {
