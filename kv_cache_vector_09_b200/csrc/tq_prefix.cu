@@ -218,51 +218,86 @@ __device__ __forceinline__ void put(__nv_bfloat16* o, float v) { *o = __float2bf
 __device__ __forceinline__ void put(__half* o, float v) { *o = __float2half_rn(v); }
 
 // Merge of one query row's partials: the block's warps take chunks in turn,
-// warp 0 adds the warps' sums in order, applies the values' QJL term and the
-// inverse rotation, and writes the row in its type.
+// four at a time so that their loads overlap, each with its own maximum; warp 0
+// merges the warps' sums in order, applies the values' QJL term and the inverse
+// rotation, and writes the row in its type.  Launched as a programmatic
+// dependent of the attention kernel.
 template <int VPL, typename TOut>
 __global__ void __launch_bounds__(kThreads)
     prefix_combine_kernel(const tq_params vp, const float* __restrict__ partials, const int nslot,
                           TOut* __restrict__ out, float* __restrict__ lse) {
-  constexpr int d = 32 * VPL;
-  __shared__ float s_acc[kWarps][d], s_as[kWarps][128], s_den[kWarps];
+  constexpr int d = 32 * VPL, kBatch = 4;
+  __shared__ float s_acc[kWarps][d], s_as[kWarps][128], s_den[kWarps], s_m[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x, vm = vp.m, ps = d + 2 + vm;
   const float* pr = partials + (size_t)row * nslot * ps;
-  float M = -INFINITY;
-  for (int c = lane; c < nslot; c += 32) M = fmaxf(M, pr[(size_t)c * ps + d]);
-  M = tq_warp_max(M);
-  const float ref = M == -INFINITY ? 0.f : M;
-  float acc[VPL], as[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
+  float acc[VPL], as[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f, M = -INFINITY;
 #pragma unroll
   for (int k = 0; k < VPL; ++k) acc[k] = 0.f;
-  for (int c = warp; c < nslot; c += kWarps) {
-    const float* pc = pr + (size_t)c * ps;
-    const float z = pc[d + 1];
-    if (z == 0.f) continue;  // an empty chunk: nothing of it but z and the maximum is defined
-    const float w = exp2f(pc[d] - ref);
-    den = fmaf(z, w, den);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int c0 = warp; c0 < nslot; c0 += kBatch * kWarps) {
+    float m[kBatch], z[kBatch], x[kBatch][VPL];
 #pragma unroll
-    for (int k = 0; k < VPL; ++k) acc[k] = fmaf(pc[lane + 32 * k], w, acc[k]);
+    for (int u = 0; u < kBatch; ++u) {
+      const int c = c0 + u * kWarps;
+      const bool on = c < nslot;
+      const float* pc = pr + (size_t)(on ? c : c0) * ps;
+      m[u] = on ? pc[d] : -INFINITY;
+      z[u] = on ? pc[d + 1] : 0.f;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (32 * u < vm) as[u] = fmaf(pc[d + 2 + lane + 32 * u], w, as[u]);
+      for (int k = 0; k < VPL; ++k) x[u][k] = pc[lane + 32 * k];
+    }
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) top = fmaxf(top, m[u]);
+    const float ref = top == -INFINITY ? 0.f : top, old = exp2f(M - ref);
+    den *= old;
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) acc[k] *= old;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) as[u] *= old;
+    M = top;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (z[u] == 0.f) continue;  // an empty chunk: nothing of it but z and the maximum is defined
+      const float w = exp2f(m[u] - ref);
+      den = fmaf(z[u], w, den);
+#pragma unroll
+      for (int k = 0; k < VPL; ++k) acc[k] = fmaf(x[u][k], w, acc[k]);
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (32 * v < vm) as[v] = fmaf(pr[(size_t)(c0 + u * kWarps) * ps + d + 2 + lane + 32 * v], w, as[v]);
+    }
   }
 #pragma unroll
   for (int k = 0; k < VPL; ++k) s_acc[warp][lane + 32 * k] = acc[k];
 #pragma unroll
   for (int u = 0; u < 4; ++u)
     if (32 * u < vm) s_as[warp][lane + 32 * u] = as[u];
-  if (lane == 0) s_den[warp] = den;
+  if (lane == 0) {
+    s_den[warp] = den;
+    s_m[warp] = M;
+  }
   __syncthreads();
   if (warp != 0) return;
-  for (int w = 1; w < kWarps; ++w) {
-    den += s_den[w];
+  M = s_m[0];
 #pragma unroll
-    for (int k = 0; k < VPL; ++k) acc[k] += s_acc[w][lane + 32 * k];
+  for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  den = 0.f;
+#pragma unroll
+  for (int k = 0; k < VPL; ++k) acc[k] = 0.f;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) as[u] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const float f = exp2f(s_m[w] - ref);  // 0 for a warp without keys, whose sums are 0 too
+    den = fmaf(s_den[w], f, den);
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) acc[k] = fmaf(s_acc[w][lane + 32 * k], f, acc[k]);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (32 * u < vm) as[u] += s_as[w][lane + 32 * u];
+      if (32 * u < vm) as[u] = fmaf(s_as[w][lane + 32 * u], f, as[u]);
   }
   if (lse && lane == 0) lse[row] = (ref + log2f(den)) * 0.693147180559945309f;
   const float inv = den == 0.f ? 0.f : 1.0f / den;  // a row without keys: zeros
@@ -303,18 +338,29 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+template <int VPL, typename TOut>
+cudaError_t launch_combine_t(const tq_params& vp, const tq_prefix_args& a, int nslot, void* out, float* lse,
+                             cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(a.B * a.Hq));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefix_combine_kernel<VPL, TOut>, vp, (const float*)a.partials, nslot, (TOut*)out, lse);
+}
+
 template <int VPL>
 cudaError_t launch_combine(const tq_params& vp, const tq_prefix_args& a, int nslot, void* out, tq_dtype dt, float* lse,
                            cudaStream_t st) {
-  const unsigned grid = (unsigned)(a.B * a.Hq);
   switch (dt) {
-    case TQ_F32: prefix_combine_kernel<VPL, float><<<grid, kThreads, 0, st>>>(vp, a.partials, nslot, (float*)out, lse); break;
-    case TQ_BF16:
-      prefix_combine_kernel<VPL, __nv_bfloat16><<<grid, kThreads, 0, st>>>(vp, a.partials, nslot, (__nv_bfloat16*)out, lse);
-      break;
-    default: prefix_combine_kernel<VPL, __half><<<grid, kThreads, 0, st>>>(vp, a.partials, nslot, (__half*)out, lse);
+    case TQ_F32: return launch_combine_t<VPL, float>(vp, a, nslot, out, lse, st);
+    case TQ_BF16: return launch_combine_t<VPL, __nv_bfloat16>(vp, a, nslot, out, lse, st);
+    default: return launch_combine_t<VPL, __half>(vp, a, nslot, out, lse, st);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace

@@ -135,7 +135,7 @@ struct Smem {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], pair[4], ofull, oempty, qfull, done;
   uint32_t tmem;
   int abort;
-  alignas(16) float a[4][kKeys], b[4][kKeys], v[4][kKeys];   // per key: a_k, b_k, nu_v 2^(14 - e)
+  alignas(16) float a[4][kKeys], b[4][kKeys], c[4][kKeys], v[4][kKeys];  // per key: a_k, b_k, 0 (-inf: no key), nu_v 2^(14 - e)
   float smax[2][2][kRows];                                   // a half tile's maximum
   float zsum[2][kRows];
   float f[8];                                                // 2^(e - 14) of a tile
@@ -157,6 +157,8 @@ struct Layout {
     kstage = sg + kKeys * m * 2;
     v = k + 2 * kstage;
     total = v + VST * NP * kpart;
+    const int rows_out = kRows * (D + 3) * 4;  // the block's result, over the same bytes
+    if (total < rows_out) total = rows_out;
   }
 };
 
@@ -164,19 +166,18 @@ struct Layout {
 // `dst` + 1024 s (and the low parts at dst + lo_off)
 template <int P, bool SPLIT>
 __device__ __forceinline__ void expand32(const uint32_t (&pl)[4], const Tab& t, unsigned char* dst, int lo_off) {
+  const uint32_t neg = ~pl[3];  // P = 4: the top bit is the sign, the others the magnitude or its complement
   uint32_t w[3];
 #pragma unroll
-  for (int p = 0; p < 3; ++p) w[p] = p < P ? (P == 4 ? ~(pl[p] ^ pl[3]) : pl[p]) : 0u;
+  for (int p = 0; p < 3; ++p) w[p] = P == 4 ? pl[p] ^ neg : pl[p];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     uint32_t sel = 0u;
 #pragma unroll
-    for (int p = 0; p < (P < 3 ? P : 3); ++p) {
-      const uint32_t x = s >= p ? w[p] >> (s - p) : w[p] << (p - s);
-      sel |= x & (0x11111111u << p);
-    }
-    uint32_t neg = 0u;  // 4 in the nibble of a negative coordinate
-    if constexpr (P == 4) neg = (s >= 2 ? ~pl[3] >> (s - 2) : ~pl[3] << (2 - s)) & 0x44444444u;
+    for (int p = 0; p < (P < 3 ? P : 3); ++p)
+      sel |= (s >= p ? w[p] >> (s - p) : w[p] << (p - s)) & (0x11111111u << p);
+    uint32_t sgn = 0u;  // 4 in a negative coordinate's nibble
+    if constexpr (P == 4) sgn = (s >= 2 ? neg >> (s - 2) : neg << (2 - s)) & 0x44444444u;
     uint4 hi, lo;
     uint32_t* ph = reinterpret_cast<uint32_t*>(&hi);
     uint32_t* pw = reinterpret_cast<uint32_t*>(&lo);
@@ -184,7 +185,7 @@ __device__ __forceinline__ void expand32(const uint32_t (&pl)[4], const Tab& t, 
     for (int h = 0; h < 2; ++h) {
       const uint32_t sl = h ? sel >> 16 : sel;
       uint32_t sg = 0u;
-      if constexpr (P == 4) sg = prmt(0u, 0x80808080u, h ? neg >> 16 : neg);
+      if constexpr (P == 4) sg = prmt(0u, 0x80808080u, h ? sgn >> 16 : sgn);
       const uint32_t a = prmt(t.hl[0], t.hl[1], sl), b = prmt(t.hh[0], t.hh[1], sl) ^ sg;
       ph[2 * h] = prmt(a, b, 0x5140);
       ph[2 * h + 1] = prmt(a, b, 0x7362);
@@ -279,11 +280,15 @@ __global__ void __launch_bounds__(256)
   __shared__ __align__(16) float qt[D][kPrepRows];  // q' transposed
   __shared__ float wt[128][kPrepRows + 1];          // S q' transposed
   __shared__ float buf[8][D], s_up[kPrepRows];
+  extern __shared__ __align__(16) float sk[];  // transposed sketch [D][m]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nrb = (B + SB - 1) / SB;
   const int part = blockIdx.x % (kRows / kPrepRows), grp = blockIdx.x / (kRows / kPrepRows);
   const int rb = grp % nrb, h = grp / nrb, m = p.m;
   const int b0 = rb * SB, rows = min(SB, B - b0) * G, r0 = part * kPrepRows;
+  for (int i = tid; i < D * m / 4; i += 256)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tqtc::smem_u32(sk + 4 * i)), "l"(p.St + 4 * i) : "memory");
+  asm volatile("cp.async.commit_group;" ::: "memory");
   for (int i = warp; i < kPrepRows; i += 8) {
     const int r = r0 + i;
     float v[VPL];
@@ -307,15 +312,16 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int k = 0; k < VPL; ++k) qt[lane + 32 * k][i] = v[k];
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
   for (int u = tid; u < 2 * m; u += 256) {
     const int c = u % m, half = u / m, Q = m / 32;
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-#pragma unroll 16
+#pragma unroll 4
     for (int i = 0; i < D; ++i) {
-      const float s = __ldg(p.St + (size_t)i * m + c);
+      const float s = sk[i * m + c];
       const float4 x = *reinterpret_cast<const float4*>(&qt[i][8 * half]);
       const float4 y = *reinterpret_cast<const float4*>(&qt[i][8 * half + 4]);
       acc[0] = fmaf(s, x.x, acc[0]);
@@ -503,44 +509,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       tqtc::tc_fence_after();
       const bool act = mine && (cur.seq < 0 || cur.seq == myseq);
       if (__any_sync(TQ_FULL_MASK, act)) {
-        const uint32_t s_col = lane_base + 128 * s2;
-        const float* ka = sm.a[j & 3] + 32 * half;
-        const float* kb = sm.b[j & 3] + 32 * half;
-        const float* kv = sm.v[j & 3] + 32 * half;
-        u64 t[16];
+        const uint32_t s_col = lane_base + 128 * s2 + 32 * half;
+        u64 t[16];  // logits over the row's scale, in pairs of keys
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int k0 = 0; k0 < 32; k0 += 16) {
           uint32_t x[16], y[16];
-          tqtc::tmem_ld16(s_col + 32 * half + k0, x);
-          if (SK) tqtc::tmem_ld16(s_col + 64 + 32 * half + k0, y);
+          tqtc::tmem_ld16(s_col + k0, x);
+          if (SK) tqtc::tmem_ld16(s_col + 64 + k0, y);
           tqtc::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const ulonglong2 a2 = *reinterpret_cast<const ulonglong2*>(ka + k0 + i);
-            u64 u0 = mul2(a2.x, pair(x[i], x[i + 1])), u1 = mul2(a2.y, pair(x[i + 2], x[i + 3]));
+          for (int i = 0; i < 4; ++i) {
+            const int k = 32 * half + k0 + 4 * i, o = k0 / 2 + 2 * i;
+            const ulonglong2 a2 = *reinterpret_cast<const ulonglong2*>(&sm.a[j & 3][k]);
+            const ulonglong2 c2 = *reinterpret_cast<const ulonglong2*>(&sm.c[j & 3][k]);
+            t[o] = fma2(a2.x, pair(x[4 * i], x[4 * i + 1]), c2.x);
+            t[o + 1] = fma2(a2.y, pair(x[4 * i + 2], x[4 * i + 3]), c2.y);
             if (SK) {
-              const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(kb + k0 + i);
-              u0 = fma2(b2.x, pair(y[i], y[i + 1]), u0);
-              u1 = fma2(b2.y, pair(y[i + 2], y[i + 3]), u1);
+              const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(&sm.b[j & 3][k]);
+              t[o] = fma2(b2.x, pair(y[4 * i], y[4 * i + 1]), t[o]);
+              t[o + 1] = fma2(b2.y, pair(y[4 * i + 2], y[4 * i + 3]), t[o + 1]);
             }
-            t[(k0 + i) / 2] = u0;
-            t[(k0 + i) / 2 + 1] = u1;
+            const float2 f = parts(t[o]), g = parts(t[o + 1]);
+            m4[i] = fmaxf(fmaxf(m4[i], fmaxf(f.x, f.y)), fmaxf(g.x, g.y));
           }
         }
-        const int64_t left = (cur.seq < 0 ? A.Tp : sm.len[cur.seq]) - cur.t0 - 32 * half;  // keys of this half tile
-        if (left < 32) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 f = parts(t[i]);
-            t[i] = pair(__float_as_uint(2 * i < left ? f.x : -INFINITY), __float_as_uint(2 * i + 1 < left ? f.y : -INFINITY));
-          }
-        }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 f = parts(t[i]);
-          mx = fmaxf(mx, fmaxf(f.x, f.y));
-        }
+        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         sm.smax[turn & 1][half][r] = mx;
         __syncwarp();
         if (lane == 0) tqtc::mbar_arrive(&sm.pair[quad]);
@@ -550,26 +544,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float ref = mx == -INFINITY ? 0.f : mx;
         const u64 rs2 = pair(rs), ref2 = pair(-ref);
         u64 z = 0ull;
-        uint32_t hi[16], lo[16];
+        // P goes over the columns of S (high parts) and R (low parts) that this
+        // warp has read
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const ulonglong2 v2 = *reinterpret_cast<const ulonglong2*>(kv + 2 * i);
+        for (int k0 = 0; k0 < 32; k0 += 16) {
+          uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const float2 e = parts(fma2(t[i + w], rs2, ref2));
-            const u64 p = pair(__float_as_uint(ex2(e.x)), __float_as_uint(ex2(e.y)));
-            z = add2(z, p);
-            const u64 pv = mul2(p, w ? v2.y : v2.x);
-            const float2 f = parts(pv);
-            hi[i + w] = pack_f16(f.x, f.y);
-            if (SPLIT) {
-              const float2 g = unpack_f16(hi[i + w]);
-              lo[i + w] = pack_f16(f.x - g.x, f.y - g.y);
+          for (int i = 0; i < 8; i += 2) {
+            const ulonglong2 v2 = *reinterpret_cast<const ulonglong2*>(&sm.v[j & 3][32 * half + k0 + 2 * i]);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const float2 e = parts(fma2(t[k0 / 2 + i + w], rs2, ref2));
+              const u64 p = pair(__float_as_uint(ex2(e.x)), __float_as_uint(ex2(e.y)));
+              z = add2(z, p);
+              const u64 pv = mul2(p, w ? v2.y : v2.x);
+              if (SPLIT) {
+                // high part: the leading 11 bits; the rest is exact in fp32
+                const u64 top = pv & 0xffffe000ffffe000ull;
+                const float2 g = parts(top), q = parts(fma2(top, pair(-1.f), pv));
+                hi[i + w] = pack_f16(g.x, g.y);
+                lo[i + w] = pack_f16(q.x, q.y);
+              } else {
+                const float2 f = parts(pv);
+                hi[i + w] = pack_f16(f.x, f.y);
+              }
             }
           }
+          tqtc::tmem_st8(s_col + k0 / 2, hi);
+          if (SPLIT) tqtc::tmem_st8(s_col + 64 + k0 / 2, lo);
         }
-        tqtc::tmem_st16(s_col + 16 * half, hi);
-        if (SPLIT) tqtc::tmem_st16(s_col + 32 + 16 * half, lo);
         tqtc::tmem_wait_st();
         if (act) {
           const float2 f = parts(z);
@@ -627,17 +630,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) tqtc::mbar_arrive(&sm.oempty);
       cur.next(sm, A.Tp);
     }
+    // rows to shared memory (the expanded tiles are spent: every product has
+    // completed), one pad word a row; the block writes them out together
     if (mine) {
-      const int qrow = (b0 + r / A.G) * A.Hq + h * A.G + r % A.G;
-      float* pr = A.partials + ((size_t)qrow * nC + c) * (D + 2);
+      float* row = reinterpret_cast<float*>(dyn) + r * (D + 3);
       const float k = vp.inv_sqrt_d / kCenScale;
 #pragma unroll
       for (int i = 0; i < NCOL / 2; ++i) {
         const float2 f = parts(acc[i]);
-        pr[coord_of(half * NCOL + 2 * i)] = f.x * k;
-        pr[coord_of(half * NCOL + 2 * i + 1)] = f.y * k;
+        row[coord_of(half * NCOL + 2 * i)] = f.x * k;
+        row[coord_of(half * NCOL + 2 * i + 1)] = f.y * k;
       }
-      if (half == 0) pr[D] = M;
+      if (half == 0) row[D] = M;
     }
   } else if (warp < kValWarp0) {
     // --------------------------------------------------- expansion of keys
@@ -648,13 +652,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int off = (key >> 3) * 128 + (key & 7) * 16;
     uint32_t kw[4][NWH], sg[2] = {0u, 0u};
     float nu = 0.f, gam = 0.f, nv0 = 0.f, nv1 = 0.f;
+    bool kvalid = false;
     auto load = [&](const Cursor& cu) {
       const bool pre = cu.seq < 0;
       const int64_t n = pre ? A.Tp : sm.len[cu.seq];
       const tq_compressed& K = pre ? A.Kp : A.K;
       const float* vn = pre ? A.Vp.norms : A.V.norms;
       const int64_t first_row = (pre ? (int64_t)h * A.Tp : ((int64_t)(b0 + cu.seq) * A.Hkv + h) * A.T) + cu.t0;
-      const bool valid = cu.t0 + key < n;
+      const bool valid = kvalid = cu.t0 + key < n;
       const int64_t row = first_row + key;
       load_planes<NWH>(kw, K.codes + row * kp.W + kw0, kp.pw, kbits, valid);
       if (SK) {
@@ -675,26 +680,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       // values was issued before, so the scalars' slot j & 3 is free
       if (j >= 2) WAIT_WARP(sm.kempty[s2], ((j >> 1) & 1) ^ 1);
       unsigned char* st = dyn + lay.k + s2 * lay.kstage;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < NWH; ++i) {
-        const uint32_t pl[4] = {kw[0][i], kw[1][i], kw[2][i], kw[3][i]};
+        const uint32_t pl[4] = {kw[0][0], kw[1][0], kw[2][0], kw[3][0]};
         expand_group<SPLIT>(kbits, pl, tk, st + (half * NWH + i) * 4096 + off, L::kpart);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) kw[p][0] = kw[p][NWH - 1];
       }
       if (SK) {
+#pragma unroll 1
+        for (int w = half; w < kp.MS; w += 2) {
+          const uint32_t y = sg[0];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int w = half + 2 * i;
-          if (w < kp.MS) {
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-              uint4 x;
-              x.x = ((sg[i] << (15 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
-              x.y = ((sg[i] << (14 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
-              x.z = ((sg[i] << (13 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
-              x.w = ((sg[i] << (12 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
-              *reinterpret_cast<uint4*>(st + lay.sg + (4 * w + ch) * 1024 + off) = x;
-            }
+          for (int ch = 0; ch < 4; ++ch) {  // pairs (j, j + 16) to the sign bits of a word
+            uint4 x;
+            x.x = ((y << (15 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
+            x.y = ((y << (14 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
+            x.z = ((y << (13 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
+            x.w = ((y << (12 - 4 * ch)) & 0x80008000u) ^ 0xBC00BC00u;
+            *reinterpret_cast<uint4*>(st + lay.sg + (4 * w + ch) * 1024 + off) = x;
           }
+          sg[0] = sg[1];
         }
       }
       if (half == 0) {
@@ -702,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = max(-100, exponent_of(nm) + 1);  // |nv| < 2^e
         sm.a[j & 3][key] = nu * ca;
         sm.b[j & 3][key] = nu * gam * cb;
+        sm.c[j & 3][key] = kvalid ? 0.f : -INFINITY;
         sm.v[j & 3][key] = ((key & 32) ? nv1 : nv0) * pow2(14 - e);
         if (key == 0) sm.f[j & 7] = pow2(e - 14);
       }
@@ -731,10 +738,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int sv = L::VST == 2 ? (j & 1) : 0, use = L::VST == 2 ? (j >> 1) : j;
       if (use >= 1) WAIT_WARP(sm.vempty[sv], (use & 1) ^ 1);
       unsigned char* st = dyn + lay.v + sv * L::NP * L::kpart;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < NWH; ++i) {
-        const uint32_t pl[4] = {vw[0][i], vw[1][i], vw[2][i], vw[3][i]};
+        const uint32_t pl[4] = {vw[0][0], vw[1][0], vw[2][0], vw[3][0]};
         expand_group<SPLIT>(vbits, pl, tv, st + (half * NWH + i) * 4096 + off, L::kpart);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) vw[p][0] = vw[p][NWH - 1];
       }
       tqtc::fence_proxy_async_smem();
       tqtc::mbar_arrive(&sm.vfull[sv]);
@@ -764,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect()) {
             const uint32_t dS = tu + 128 * s2, kst = base + lay.k + s2 * lay.kstage;
             // parts: low queries, low keys, then the high product
-#pragma unroll
+#pragma unroll 1
             for (int pr = SPLIT ? 0 : 2; pr < 3; ++pr) {
               const uint32_t qa = tu + kColQ + (pr == 0 ? D / 2 : 0);
               const uint64_t kd = tqtc::smem_desc(kst + (pr == 1 ? L::kpart : 0), 1024, 128);
@@ -774,15 +783,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (SK) {
               const uint64_t sd = tqtc::smem_desc(kst + lay.sg, 1024, 128);
-#pragma unroll
+#pragma unroll 1
               for (int pr = SPLIT ? 0 : 1; pr < 2; ++pr) {
                 const uint64_t wd = tqtc::smem_desc(base + lay.w + (pr == 0 ? kRows * kp.m * 2 : 0), 2048, 128);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if (k < ks) {
-                    tqtc::mma_f16_ss(dS + 64, wd + 512 * k, sd + 256 * k, idS, !(k == 0 && pr == (SPLIT ? 0 : 1)));
-                    tqtc::mma_f16_ss(dS + 64, wd + 512 * k + 256, sd + 256 * k + 128, idS, true);
-                  }
+#pragma unroll 1
+                for (int k = 0; k < ks; ++k) {
+                  tqtc::mma_f16_ss(dS + 64, wd + 512 * k, sd + 256 * k, idS, !(k == 0 && pr == (SPLIT ? 0 : 1)));
+                  tqtc::mma_f16_ss(dS + 64, wd + 512 * k + 256, sd + 256 * k + 128, idS, true);
                 }
               }
             }
@@ -800,13 +807,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tqtc::tc_fence_after();
           if (elect()) {
             const uint32_t dO = tu + kColO, pA = tu + 128 * s2, vst = base + lay.v + sv * L::NP * L::kpart;
-#pragma unroll
+#pragma unroll 1
             for (int pr = SPLIT ? 0 : 2; pr < 3; ++pr) {
-              const uint32_t pa = pA + (pr == 0 ? 32 : 0);
+              const uint32_t pa = pA + (pr == 0 ? 64 : 0);
               const uint64_t vd = tqtc::smem_desc(vst + (pr == 1 ? L::kpart : 0), 128, 1024);
 #pragma unroll
               for (int k = 0; k < kKeys / 16; ++k)
-                tqtc::mma_f16_ts(dO, pa + 8 * k, vd + 16 * k, idO, !(k == 0 && pr == (SPLIT ? 0 : 2)));
+                tqtc::mma_f16_ts(dO, pa + 32 * (k >> 1) + 8 * (k & 1), vd + 16 * k, idO, !(k == 0 && pr == (SPLIT ? 0 : 2)));
             }
             tqtc::mma_commit(&sm.vempty[sv]);
             tqtc::mma_commit(&sm.ofull);
@@ -824,10 +831,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tqtc::tc_fence_before();
   __syncthreads();
-  if (tid < rows) {
-    // the two halves' sums (their exponentials refer to the same maxima)
-    const int qrow = (b0 + tid / A.G) * A.Hq + h * A.G + tid % A.G;
-    A.partials[((size_t)qrow * nC + c) * (D + 2) + D + 1] = sm.zsum[0][tid] + sm.zsum[1][tid];
+  for (int r = warp; r < rows; r += kThreads / 32) {
+    float* pr = A.partials + ((size_t)((b0 + r / A.G) * A.Hq + h * A.G + r % A.G) * nC + c) * (D + 2);
+    const float* row = reinterpret_cast<const float*>(dyn) + r * (D + 3);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) pr[lane + 32 * k] = row[lane + 32 * k];
+    // the two halves' sums: their exponentials refer to the same maxima
+    if (lane < 2) pr[D + lane] = lane ? sm.zsum[0][r] + sm.zsum[1][r] : row[D];
   }
   if (warp == kMmaWarp) {
     tqtc::tc_fence_after();
@@ -835,23 +845,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+template <int D, typename TIn>
+cudaError_t launch_prep(const tq_params& kp, const tq_prefix_args& a, int SB, unsigned groups, cudaStream_t st) {
+  auto fn = prefix_prep_kernel<D, TIn>;
+  const size_t smem = sizeof(float) * (size_t)D * kp.m;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  fn<<<groups * (kRows / kPrepRows), 256, smem, st>>>(kp, (const TIn*)a.q, a.B, a.Hq, a.G, SB, a.image, a.scales);
+  return cudaGetLastError();
+}
+
 template <int D, bool SPLIT, bool SK>
 cudaError_t launch(const tq_params& kp, const tq_params& vp, const tq_prefix_args& a, int nC, int SB, unsigned groups,
                    cudaStream_t st) {
   const Layout<D, SPLIT> lay(kp.m);
   auto fn = prefix_tc_kernel<D, SPLIT, SK>;
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, lay.total);
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, lay.total);
   if (e != cudaSuccess) return e;
-  const dim3 prep(groups * (kRows / kPrepRows));
-  unsigned char* img = a.image;
-  float* sc = a.scales;
-  switch (a.dtype) {
-    case TQ_F32: prefix_prep_kernel<D, float><<<prep, 256, 0, st>>>(kp, (const float*)a.q, a.B, a.Hq, a.G, SB, img, sc); break;
-    case TQ_BF16:
-      prefix_prep_kernel<D, __nv_bfloat16><<<prep, 256, 0, st>>>(kp, (const __nv_bfloat16*)a.q, a.B, a.Hq, a.G, SB, img, sc);
-      break;
-    default: prefix_prep_kernel<D, __half><<<prep, 256, 0, st>>>(kp, (const __half*)a.q, a.B, a.Hq, a.G, SB, img, sc);
-  }
+  e = a.dtype == TQ_F32    ? launch_prep<D, float>(kp, a, SB, groups, st)
+      : a.dtype == TQ_BF16 ? launch_prep<D, __nv_bfloat16>(kp, a, SB, groups, st)
+                           : launch_prep<D, __half>(kp, a, SB, groups, st);
+  if (e != cudaSuccess) return e;
   // programmatic dependent launch: the blocks set up and expand their first
   // tiles while the queries are prepared, and wait for the image where they read it
   cudaLaunchConfig_t cfg = {};
