@@ -323,10 +323,9 @@ def _arg(t: Optional[torch.Tensor], name: str, codec: Codec, dtype, n: int) -> O
     least n elements, on the codec's device."""
     if t is None:
         return None
-    assert t.dtype == dtype, f"{name} must be {dtype} (got {t.dtype})"
-    assert t.is_contiguous(), f"{name} must be contiguous"
-    assert t.numel() >= n, f"{name} has {t.numel()} elements, {n} needed"
-    assert t.is_cuda and t.device.index == codec.device, f"{name} must be on the codec's device"
+    assert (t.dtype is dtype and t.numel() >= n and t.get_device() == codec.device and t.is_contiguous()), (
+        f"{name} must be a contiguous {dtype} tensor of at least {n} elements on cuda:{codec.device} "
+        f"(got {t.dtype}, {t.numel()} elements, {t.device}, contiguous: {t.is_contiguous()})")
     return t.data_ptr()
 
 

@@ -34,67 +34,63 @@ struct Exponent {
 
 constexpr int kMassThreads = 512;
 constexpr int kMassWarps = kMassThreads / 32;
-constexpr size_t kMassSmem = 200 * 1024;  // most logits that a block keeps
+constexpr size_t kMassSmem = 200 * 1024;  // most bytes of logits that a block keeps
+constexpr int kGivenKeys = 1024;          // keys of a block when the statistics are given
 
-// log2 of a row's sum of exponentials as hi + lo; a row without keys gives
-// nothing: 2^(x - inf) = 0
-__device__ __forceinline__ void split_stat(double stat, float& hi, float& lo) {
-  hi = stat == -INFINITY ? INFINITY : (float)stat;
-  lo = stat == -INFINITY ? 0.f : (float)(stat - (double)(float)stat);
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// mass of V consecutive keys from logits at lg (heads `pitch` apart)
-template <int V>
-__device__ __forceinline__ void mass_add(const float* lg, int64_t pitch, int G, const Exponent& ex, const float* s_hi,
-                                         const float* s_lo, float decay, float* mass) {
-  float add[V], l[V], m[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) add[i] = 0.f;
-#pragma unroll 4
-  for (int g = 0; g < G; ++g) {
-    if constexpr (V == 4) {
-      *reinterpret_cast<float4*>(l) = *reinterpret_cast<const float4*>(lg + g * pitch);
-    } else {
-      l[0] = lg[g * pitch];
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) add[i] += exp2f(ex.of(l[i], s_hi[g], s_lo[g]));
-  }
-  if constexpr (V == 4)
-    *reinterpret_cast<float4*>(m) = *reinterpret_cast<const float4*>(mass);
-  else
-    m[0] = *mass;
-#pragma unroll
-  for (int i = 0; i < V; ++i) m[i] = fmaf(m[i], decay, add[i]);
-  if constexpr (V == 4)
-    *reinterpret_cast<float4*>(mass) = *reinterpret_cast<const float4*>(m);
-  else
-    *mass = m[0];
-}
-
-// Statistics given: one pass, a thread four keys (one when T % 4 leaves the
-// rows unaligned), blocks over (sequence, KV head, piece of the keys).
-template <int V>
+// Statistics given: one pass, a thread four keys: consecutive ones by 16-byte
+// loads (VEC), or, when T % 4 leaves the rows unaligned, 256 apart.
+template <bool VEC>
 __global__ void __launch_bounds__(256)
     mass_given_kernel(const tq_params p, const float* __restrict__ logits, const int Hq, const int Hkv, const int64_t T,
                       const int32_t* __restrict__ lens, const float* __restrict__ lse, const Exponent ex,
                       const float decay, float* __restrict__ mass) {
   __shared__ float s_hi[32], s_lo[32];
-  const int64_t pieces = (T + 256 * V - 1) / (256 * V);
-  const int64_t bh = blockIdx.x / pieces, piece = blockIdx.x % pieces;
+  const int64_t pieces = (T + kGivenKeys - 1) / kGivenKeys;
+  const int64_t bh = blockIdx.x / pieces, t0 = blockIdx.x % pieces * kGivenKeys;
   const int h = (int)(bh % Hkv), b = (int)(bh / Hkv), G = Hq / Hkv;
-  const int64_t n = held_len(lens, b, T, p.err);
-  if (piece * 256 * V >= n) return;
-  if (threadIdx.x < G) split_stat((double)lse[b * Hq + h * G + threadIdx.x] * 1.4426950408889634, s_hi[threadIdx.x], s_lo[threadIdx.x]);
-  __syncthreads();
-  const float* lg = logits + ((int64_t)b * Hq + h * G) * T;
-  float* mr = mass + bh * T;
-  const int64_t t = (piece * 256 + threadIdx.x) * V;
-  if (t + V <= n) {
-    mass_add<V>(lg + t, T, G, ex, s_hi, s_lo, decay, mr + t);
-  } else {
-    for (int64_t u = t; u < n; ++u) mass_add<1>(lg + u, T, G, ex, s_hi, s_lo, decay, mr + u);
+  if (threadIdx.x < G) {
+    // ln to log2 units, in two parts; a row without keys gives nothing: 2^(x - inf) = 0
+    const double stat = (double)lse[b * Hq + h * G + threadIdx.x] * 1.4426950408889634;
+    s_hi[threadIdx.x] = stat == -INFINITY ? INFINITY : (float)stat;
+    s_lo[threadIdx.x] = stat == -INFINITY ? 0.f : (float)(stat - (double)(float)stat);
   }
+  const int64_t n = held_len(lens, b, T, p.err);
+  if (t0 >= n) return;
+  __syncthreads();
+  const float* lg = logits + ((int64_t)b * Hq + h * G) * T + t0;
+  float* mr = mass + bh * T + t0;
+  const int left = (int)min((int64_t)kGivenKeys, n - t0), tid = threadIdx.x;
+  float add[4] = {0.f, 0.f, 0.f, 0.f};
+  if (VEC && 4 * tid + 4 <= left) {
+    const float4 m = *reinterpret_cast<const float4*>(mr + 4 * tid);
+#pragma unroll 4
+    for (int g = 0; g < G; ++g) {
+      const float4 l = __ldg(reinterpret_cast<const float4*>(lg + g * T) + tid);
+      add[0] += ex2(ex.of(l.x, s_hi[g], s_lo[g]));
+      add[1] += ex2(ex.of(l.y, s_hi[g], s_lo[g]));
+      add[2] += ex2(ex.of(l.z, s_hi[g], s_lo[g]));
+      add[3] += ex2(ex.of(l.w, s_hi[g], s_lo[g]));
+    }
+    *reinterpret_cast<float4*>(mr + 4 * tid) = make_float4(fmaf(m.x, decay, add[0]), fmaf(m.y, decay, add[1]),
+                                                           fmaf(m.z, decay, add[2]), fmaf(m.w, decay, add[3]));
+    return;
+  }
+  const int first = VEC ? 4 * tid : tid, step = VEC ? 1 : 256;
+#pragma unroll 2
+  for (int g = 0; g < G; ++g) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (first + i * step < left) add[i] += ex2(ex.of(__ldg(lg + g * T + first + i * step), s_hi[g], s_lo[g]));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (first + i * step < left) mr[first + i * step] = fmaf(mr[first + i * step], decay, add[i]);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -110,104 +106,151 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// a float in the shared memory of block `rank` of the cluster
-__device__ __forceinline__ float peer_ld(const float* p, uint32_t rank) {
-  uint32_t a;
-  float v;
+// a word in the shared memory of block `rank` of the cluster
+__device__ __forceinline__ uint32_t peer_ld(const void* p, uint32_t rank) {
+  uint32_t a, v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
 
 // No statistics given: a cluster of blocks takes one (sequence, KV head), each
-// an equal part of its keys.  A block brings its part of the G rows into shared
-// memory once, leaves each row's maximum and sum of exponentials, and after one
-// exchange over the cluster adds the weights: the logits are read once from
-// memory.  A part that does not fit (KEEP false) is read again through the L2.
+// an equal part of its keys, and each warp of a block one head's logits over a
+// piece of that part: it fetches them into shared memory (KEEP), leaves the
+// piece's maximum m and sum z = sum 2^(l - m), and 2^(l - m) in the logits'
+// place.  After one exchange over the cluster the weight of a key is that
+// exponential times the piece's factor 2^(m - M) / Z: the logits are read once
+// and exponentiated once.  A part that does not fit is read again through the
+// L2 and exponentiated twice.
 template <int V, bool KEEP>
 __global__ void __launch_bounds__(kMassThreads)
     mass_kernel(const tq_params p, const float* __restrict__ logits, const int Hq, const int Hkv, const int64_t T,
                 const int32_t* __restrict__ lens, const Exponent ex, const float decay, float* __restrict__ mass) {
   extern __shared__ __align__(16) float keep[];
-  __shared__ float s_hi[32], s_lo[32], s_red[32][kMassWarps], s_m[32], s_z[32];
+  __shared__ float s_m[32][kMassWarps], s_z[32][kMassWarps], s_f[32][kMassWarps];
+  __shared__ float s_bm[32], s_bz[32], s_M[32], s_rz[32];
   const uint32_t rank = cluster_rank(), C = cluster_size();
   const int64_t bh = blockIdx.x / C;
   const int h = (int)(bh % Hkv), b = (int)(bh / Hkv), G = Hq / Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t n = held_len(lens, b, T, p.err);
   const int64_t per = ((n + C - 1) / C + 3) & ~(int64_t)3;
-  const int64_t t0 = min(n, rank * per), len = min(n, t0 + per) - t0;
+  const int64_t t0 = min(n, rank * per);
+  const int len = (int)(min(n, t0 + per) - t0);
   const float* lg = logits + ((int64_t)b * Hq + h * G) * T + t0;
-  int64_t pitch = T;
+  const int nsub = G >= kMassWarps ? 1 : kMassWarps / G;         // pieces a head
+  const int ps = ((len + nsub - 1) / nsub + 3) & ~3;             // keys a piece
+  const int units = G * nsub;
   if constexpr (KEEP) {
-    pitch = per;
-    const int64_t cnt = (len + V - 1) / V;  // copies a row: the last of four covers the row's end
-    for (int g = 0; g < G; ++g) {
-      for (int64_t i = tid; i < cnt; i += kMassThreads) {
-        const uint32_t dst = (uint32_t)__cvta_generic_to_shared(keep + g * per + i * V);
-        const float* src = lg + g * T + i * V;
-        if (V == 4 && i * 4 + 4 <= len) {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    for (int u = warp; u < units; u += kMassWarps) {
+      const int g = u / nsub, k0 = min(len, u % nsub * ps), k1 = min(len, k0 + ps);
+      float* dst = keep + (size_t)g * per;
+      const float* src = lg + g * T;
+      for (int k = k0 + lane * V; k < k1; k += 32 * V) {
+        if (V == 4 && k + 4 <= k1) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst + k)), "l"(src + k) : "memory");
         } else {
-          for (int64_t u = i * V; u < len && u < i * V + V; ++u)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + (uint32_t)(u - i * V) * 4), "l"(lg + g * T + u) : "memory");
+          for (int q = k; q < min(k1, k + V); ++q)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst + q)), "l"(src + q) : "memory");
         }
       }
     }
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-    lg = keep;
-    __syncthreads();
+    __syncwarp();
   }
-  for (int g = 0; g < G; ++g) {
-    float mx = -INFINITY;
+  for (int u = warp; u < units; u += kMassWarps) {
+    const int g = u / nsub, sub = u % nsub, k0 = min(len, sub * ps), k1 = min(len, k0 + ps);
+    float* row = keep + (size_t)g * per;
+    const float* src = KEEP ? row : lg + g * T;
+    float mx = -INFINITY, z = 0.f;
 #pragma unroll 8
-    for (int64_t t = tid; t < len; t += kMassThreads) mx = fmaxf(mx, lg[g * pitch + t]);
+    for (int k = k0 + lane; k < k1; k += 32) mx = fmaxf(mx, src[k]);
     mx = tq_warp_max(mx);
-    if (lane == 0) s_red[g][warp] = mx;
-  }
-  __syncthreads();
-  if (tid < G) {
-    float mx = -INFINITY;
-    for (int w = 0; w < kMassWarps; ++w) mx = fmaxf(mx, s_red[tid][w]);
-    s_m[tid] = mx;
-  }
-  __syncthreads();
-  for (int g = 0; g < G; ++g) {
-    const float mx = s_m[g] == -INFINITY ? 0.f : s_m[g];
-    float z = 0.f;
+    const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll 8
-    for (int64_t t = tid; t < len; t += kMassThreads) z += exp2f((lg[g * pitch + t] - mx) * ex.ch);
+    for (int k = k0 + lane; k < k1; k += 32) {
+      const float e = ex2((src[k] - ref) * ex.ch);
+      z += e;
+      if (KEEP) row[k] = e;
+    }
     z = tq_warp_sum(z);
-    if (lane == 0) s_red[g][warp] = z;
+    if (lane == 0) {
+      s_m[g][sub] = mx;
+      s_z[g][sub] = z;
+    }
   }
   __syncthreads();
   if (tid < G) {
-    float z = 0.f;
-    for (int w = 0; w < kMassWarps; ++w) z += s_red[tid][w];
-    s_z[tid] = z;
+    float mx = -INFINITY, z = 0.f;
+    for (int q = 0; q < nsub; ++q) mx = fmaxf(mx, s_m[tid][q]);
+    for (int q = 0; q < nsub; ++q)
+      if (s_z[tid][q] != 0.f) z += s_z[tid][q] * ex2((s_m[tid][q] - mx) * ex.ch);
+    s_bm[tid] = mx;
+    s_bz[tid] = z;
   }
   cluster_sync();
   if (tid < G) {
-    float mx = -INFINITY;
-    for (uint32_t r = 0; r < C; ++r) mx = fmaxf(mx, peer_ld(&s_m[tid], r));
-    double z = 0.0;
-    for (uint32_t r = 0; r < C; ++r) {
-      const float m = peer_ld(&s_m[tid], r);
-      const float zr = peer_ld(&s_z[tid], r);
-      if (m != -INFINITY || zr != 0.f) z += (double)zr * exp2((double)(m - mx) * (double)ex.ch);
+    float mx = -INFINITY, z = 0.f, m[8], zr[8];
+#pragma unroll
+    for (uint32_t r = 0; r < 8; ++r) {
+      m[r] = r < C ? __uint_as_float(peer_ld(&s_bm[tid], r)) : -INFINITY;
+      zr[r] = r < C ? __uint_as_float(peer_ld(&s_bz[tid], r)) : 0.f;
+      mx = fmaxf(mx, m[r]);
     }
-    // all masked: nothing to add
-    split_stat(mx == -INFINITY && z == 0.0 ? -INFINITY : (double)mx * ((double)ex.ch + (double)ex.cl) + log2(z), s_hi[tid], s_lo[tid]);
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      if (zr[r] != 0.f) z += zr[r] * ex2((m[r] - mx) * ex.ch);
+    s_M[tid] = mx == -INFINITY ? 0.f : mx;
+    s_rz[tid] = z == 0.f ? 0.f : 1.f / z;  // all masked: nothing to add
   }
-  cluster_sync();  // nobody leaves while its statistics may be read
+  cluster_sync();  // also: nobody leaves while its statistics may be read
+  for (int u = tid; u < units; u += kMassThreads) {
+    const int g = u / nsub, sub = u % nsub;
+    s_f[g][sub] = s_z[g][sub] == 0.f ? 0.f : ex2((s_m[g][sub] - s_M[g]) * ex.ch) * s_rz[g];
+  }
+  __syncthreads();
   float* mr = mass + bh * T + t0;
-  if (V == 4) {
-    for (int64_t t = (int64_t)tid * 4; t + 4 <= len; t += kMassThreads * 4)
-      mass_add<4>(lg + t, pitch, G, ex, s_hi, s_lo, decay, mr + t);
-    const int64_t tail = len & ~(int64_t)3;
-    if (tid < len - tail) mass_add<1>(lg + tail + tid, pitch, G, ex, s_hi, s_lo, decay, mr + tail + tid);
-  } else {
-    for (int64_t t = tid; t < len; t += kMassThreads) mass_add<1>(lg + t, pitch, G, ex, s_hi, s_lo, decay, mr + t);
+  for (int k = tid * V; k < len; k += kMassThreads * V) {
+    float add[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) add[i] = 0.f;
+    const int sub = KEEP ? k / ps : 0;  // ps % 4 = 0: the V keys are of one piece
+    if (V == 4 && k + 4 <= len) {
+      float4 m = *reinterpret_cast<const float4*>(mr + k);
+#pragma unroll 4
+      for (int g = 0; g < G; ++g) {
+        float4 e;
+        float f;
+        if constexpr (KEEP) {
+          e = *reinterpret_cast<const float4*>(keep + (size_t)g * per + k);
+          f = s_f[g][sub];
+        } else {
+          e = __ldg(reinterpret_cast<const float4*>(lg + g * T + k));
+          const float M = s_M[g];
+          e = make_float4(ex2((e.x - M) * ex.ch), ex2((e.y - M) * ex.ch), ex2((e.z - M) * ex.ch), ex2((e.w - M) * ex.ch));
+          f = s_rz[g];
+        }
+        add[0] = fmaf(e.x, f, add[0]);
+        add[V > 1 ? 1 : 0] = fmaf(e.y, f, add[V > 1 ? 1 : 0]);
+        add[V > 2 ? 2 : 0] = fmaf(e.z, f, add[V > 2 ? 2 : 0]);
+        add[V > 3 ? 3 : 0] = fmaf(e.w, f, add[V > 3 ? 3 : 0]);
+      }
+      m = make_float4(fmaf(m.x, decay, add[0]), fmaf(m.y, decay, add[V > 1 ? 1 : 0]),
+                      fmaf(m.z, decay, add[V > 2 ? 2 : 0]), fmaf(m.w, decay, add[V > 3 ? 3 : 0]));
+      *reinterpret_cast<float4*>(mr + k) = m;
+    } else {
+      for (int q = k; q < min(len, k + V); ++q) {
+        float a = 0.f;
+#pragma unroll 4
+        for (int g = 0; g < G; ++g) {
+          if constexpr (KEEP)
+            a = fmaf(keep[(size_t)g * per + q], s_f[g][sub], a);
+          else
+            a = fmaf(ex2((__ldg(lg + g * T + q) - s_M[g]) * ex.ch), s_rz[g], a);
+        }
+        mr[q] = fmaf(mr[q], decay, a);
+      }
+    }
   }
 }
 
@@ -219,69 +262,77 @@ __device__ __forceinline__ uint32_t mass_key(float v) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-constexpr int kEvThreads = 1024;
+constexpr int kEvThreads = 512;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvKeep = 50 * 1024;  // most keys that a block keeps in shared memory
 
-// One block: one (sequence, KV head).  A radix selection over the keys between
-// the sinks and the recent ones, eleven, eleven and ten bits, finds the
-// smallest kept key and how many of its equals stay (the lowest indices); then
-// every warp counts what stays in its contiguous piece, and after one scan
-// over the warps writes it in order.  The masses are read once and kept as
-// ordered keys in shared memory when they fit (KEEP).
+// sum of the first `warp` of kEvWarps counters, by one load and five shuffles
+__device__ __forceinline__ int before_warp(const int* s, int warp, int lane) {
+  return tq_warp_sum(lane < warp ? s[lane] : 0);
+}
+
+// A cluster of blocks: one (sequence, KV head), each block a contiguous part
+// of its keys.  A radix selection over the keys between the sinks and the
+// recent ones, eleven, eleven and ten bits, finds the smallest kept key and how
+// many of its equals stay (the lowest indices): every block counts its part's
+// digits and sums the counters of all.  Then every warp counts what stays in
+// its contiguous piece, and after one scan over warps and blocks writes it in
+// order.  The masses are read once and kept as ordered keys in shared memory
+// when they fit (KEEP).
 template <bool KEEP>
 __global__ void __launch_bounds__(kEvThreads)
     evict_kernel(const tq_params p, const float* __restrict__ mass, const int Hkv, const int64_t T,
                  const int32_t* __restrict__ lens, const int64_t keep, const int64_t sink, const int64_t recent,
                  int32_t* __restrict__ idx, float* __restrict__ mass_out, int32_t* __restrict__ lens_out) {
   extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ int s_hist[2048], s_sum[kEvWarps];
-  __shared__ int64_t s_at[kEvWarps], s_tie[kEvWarps];
+  __shared__ int s_hist[3][2048], s_sum[kEvWarps], s_sure[kEvWarps], s_equal[kEvWarps], s_total[2], s_need;
   __shared__ uint32_t s_key;
-  __shared__ int s_need;
-  const int b = blockIdx.x / Hkv, h = blockIdx.x % Hkv;
+  const uint32_t rank = cluster_rank(), C = cluster_size();
+  const int64_t bh = blockIdx.x / C;
+  const int b = (int)(bh / Hkv), h = (int)(bh % Hkv);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t n = held_len(lens, b, T, p.err);
-  const float* mr = mass + (int64_t)blockIdx.x * T;
-  int32_t* ir = idx + (int64_t)blockIdx.x * keep;
-  float* mo = mass_out ? mass_out + (int64_t)blockIdx.x * keep : nullptr;
+  const float* mr = mass + bh * T;
+  int32_t* ir = idx + bh * keep;
+  float* mo = mass_out ? mass_out + bh * keep : nullptr;
   const int64_t kept = n < keep ? n : keep;
-  if (h == 0 && tid == 0 && lens_out) lens_out[b] = (int32_t)kept;
-  for (int64_t i = kept + tid; i < keep; i += kEvThreads) {
+  if (rank == 0 && h == 0 && tid == 0 && lens_out) lens_out[b] = (int32_t)kept;
+  for (int64_t i = kept + rank * kEvThreads + tid; i < keep; i += C * kEvThreads) {
     ir[i] = -1;
     if (mo) mo[i] = 0.f;
   }
-  if (n <= keep) {
-    for (int64_t i = tid; i < n; i += kEvThreads) {
+  if (n <= keep) {  // for all blocks of the cluster alike
+    for (int64_t i = rank * kEvThreads + tid; i < n; i += C * kEvThreads) {
       ir[i] = (int32_t)i;
       if (mo) mo[i] = mr[i];
     }
     return;
   }
   const int64_t lo = sink, hi = n - recent;  // the keys to choose from: more than `need` of them
+  const int64_t part = ((n + C - 1) / C + 31) & ~(int64_t)31;
+  const int64_t p0 = min(n, rank * part), p1 = min(n, p0 + part);
   if (KEEP) {
 #pragma unroll 8
-    for (int64_t t = tid; t < n; t += kEvThreads) keys[t] = mass_key(mr[t]);
+    for (int64_t t = p0 + tid; t < p1; t += kEvThreads) keys[t - p0] = mass_key(__ldg(mr + t));
   }
-  auto key_of = [&](int64_t t) { return KEEP ? keys[t] : mass_key(mr[t]); };
-  if (tid == 0) {
-    s_key = 0u;
-    s_need = (int)(keep - sink - recent);
-  }
+  for (int i = tid; i < 3 * 2048; i += kEvThreads) (&s_hist[0][0])[i] = 0;
+  auto key_of = [&](int64_t t) { return KEEP ? keys[t - p0] : mass_key(__ldg(mr + t)); };
+  int need = (int)(keep - sink - recent);
+  uint32_t key = 0u;
+  const bool any = need > 0;
   __syncthreads();
-  const bool any = s_need > 0;
   if (any) {
+    const int64_t c0 = max(lo, p0), c1 = min(hi, p1);
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, digits = pass == 2 ? 1024 : 2048;
-      for (int i = tid; i < digits; i += kEvThreads) s_hist[i] = 0;
-      __syncthreads();
-      const uint32_t want = s_key, above = pass == 0 ? 0u : 0xffffffffu << (pass == 1 ? 21 : 10);
-      const int need = s_need;
-      for (int64_t t0 = lo; t0 < hi; t0 += kEvThreads) {
-        const int64_t t = t0 + tid;
-        const uint32_t k = t < hi ? key_of(t) : 0u;
-        const bool in = t < hi && (k & above) == want;
+      const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (pass == 1 ? 21 : 10);
+      int* hist = s_hist[pass];
+#pragma unroll 2
+      for (int64_t t0 = c0 + warp * 32; t0 < c1; t0 += kEvThreads) {
+        const int64_t t = t0 + lane;
+        const uint32_t k = t < c1 ? key_of(t) : 0u;
+        const bool in = t < c1 && (k & above) == key;
         const int digit = (int)(k >> shift) & (digits - 1);
         // lanes with the first lane's digit count as one: untouched keys, all
         // of mass 0, would otherwise queue at a single counter
@@ -289,15 +340,21 @@ __global__ void __launch_bounds__(kEvThreads)
         if (on == 0u) continue;
         const int lead = __shfl_sync(TQ_FULL_MASK, digit, __ffs(on) - 1);
         const uint32_t same = __ballot_sync(TQ_FULL_MASK, in && digit == lead);
-        if (lane == __ffs(on) - 1) atomicAdd(&s_hist[lead], __popc(same));
-        if (in && digit != lead) atomicAdd(&s_hist[digit], 1);
+        if (lane == __ffs(on) - 1) atomicAdd(&hist[lead], __popc(same));
+        if (in && digit != lead) atomicAdd(&hist[digit], 1);
       }
-      __syncthreads();
-      // the digit where the count from the top passes `need`: thread i sums
-      // `digits` / 1024 counters from the top, then a scan over the block
-      const int each = digits / kEvThreads, d0 = digits - 1 - tid * each;
-      const int c0 = s_hist[d0], c1 = each == 2 ? s_hist[d0 - 1] : 0;
-      int x = c0 + c1;
+      cluster_sync();
+      // the digit where the count from the top passes `need`: a thread sums
+      // digits / 512 counters from the top, then a scan over the block
+      const int each = digits / kEvThreads, top = digits - 1 - tid * each;
+      int c[4] = {0, 0, 0, 0}, x = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < each) {
+          for (uint32_t r = 0; r < C; ++r) c[q] += (int)peer_ld(&hist[top - q], r);
+          x += c[q];
+        }
+      const int own = x;
 #pragma unroll
       for (int s = 1; s < 32; s <<= 1) {
         const int y = __shfl_up_sync(TQ_FULL_MASK, x, s);
@@ -305,44 +362,54 @@ __global__ void __launch_bounds__(kEvThreads)
       }
       if (lane == 31) s_sum[warp] = x;
       __syncthreads();
-      int base = 0;
-      for (int w = 0; w < warp; ++w) base += s_sum[w];
-      const int before = base + x - c0 - c1;  // greater digits than this thread's
-      if (before < need && need <= before + c0) {
-        s_key = want | ((uint32_t)d0 << shift);
-        s_need = need - before;
-      } else if (before + c0 < need && need <= before + c0 + c1) {
-        s_key = want | ((uint32_t)(d0 - 1) << shift);
-        s_need = need - before - c0;
-      }
+      int before = before_warp(s_sum, warp, lane) + x - own;  // greater digits than this thread's
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < each) {
+          if (before < need && need <= before + c[q]) {
+            s_key = key | ((uint32_t)(top - q) << shift);
+            s_need = need - before;
+          }
+          before += c[q];
+        }
       __syncthreads();
+      key = s_key;
+      need = s_need;
     }
   }
-  const uint32_t key = s_key;
-  const int64_t ties = any ? s_need : 0;  // of the keys equal to `key`
+  const int ties = any ? need : 0;  // of the keys equal to `key`
   // a warp's contiguous piece: what stays for certain, and how many equal `key`
-  const int64_t per = ((n + kEvWarps - 1) / kEvWarps + 31) & ~(int64_t)31;
-  const int64_t w0 = min(n, warp * per), w1 = min(n, w0 + per);
+  const int64_t per = (((p1 - p0) + kEvWarps - 1) / kEvWarps + 31) & ~(int64_t)31;
+  const int64_t w0 = min(p1, p0 + warp * per), w1 = min(p1, w0 + per);
   int sure = 0, equal = 0;
-  for (int64_t t0 = w0; t0 < w1; t0 += 32) {
-    const int64_t t = t0 + lane;
-    const bool on = t < w1, mid = t >= lo && t < hi;
-    const uint32_t k = on ? key_of(t) : 0u;
-    sure += on && (!mid || (any && k > key));
-    equal += on && mid && any && k == key;
+#pragma unroll 4
+  for (int64_t t = w0 + lane; t < w1; t += 32) {
+    const bool mid = t >= lo && t < hi;
+    const uint32_t k = key_of(t);
+    sure += !mid || (any && k > key);
+    equal += mid && any && k == key;
   }
   sure = tq_warp_sum(sure);
   equal = tq_warp_sum(equal);
   if (lane == 0) {
-    s_at[warp] = sure;
-    s_tie[warp] = equal;
+    s_sure[warp] = sure;
+    s_equal[warp] = equal;
   }
   __syncthreads();
-  int64_t at = 0, tied = 0;
-  for (int w = 0; w < warp; ++w) {
-    at += s_at[w];
-    tied += s_tie[w];
+  if (warp == 0) {
+    const int a = tq_warp_sum(lane < kEvWarps ? s_sure[lane] : 0), e = tq_warp_sum(lane < kEvWarps ? s_equal[lane] : 0);
+    if (lane == 0) {
+      s_total[0] = a;
+      s_total[1] = e;
+    }
   }
+  cluster_sync();
+  int at = before_warp(s_sure, warp, lane), tied = before_warp(s_equal, warp, lane);
+  for (uint32_t r = 0; r < rank; ++r) {
+    at += (int)peer_ld(&s_total[0], r);
+    tied += (int)peer_ld(&s_total[1], r);
+  }
+  cluster_sync();  // nobody leaves while its counters may be read
   at += min(tied, ties);  // the equal ones that stay before this piece
   for (int64_t t0 = w0; t0 < w1; t0 += 32) {
     const int64_t t = t0 + lane;
@@ -355,7 +422,7 @@ __global__ void __launch_bounds__(kEvThreads)
     if (stay) {
       const int64_t o = at + __popc(bs & below);
       ir[o] = (int32_t)t;
-      if (mo) mo[o] = mr[t];
+      if (mo) mo[o] = __ldg(mr + t);
     }
     at += __popc(bs);
     tied += __popc(be);
@@ -422,6 +489,25 @@ void launch_copy(const tq_params& p, const tq_compressed& src, int64_t src_T, co
   copy_rows_kernel<VC, VS><<<grid, 256, 0, st>>>(p, src, src_T, dst, dst_T, total, n, src_idx, dst_idx, mc, ms);
 }
 
+template <typename... P, typename... A>
+cudaError_t launch_cluster(void (*fn)(P...), int64_t units, int C, int threads, size_t smem, size_t most,
+                           cudaStream_t st, A... args) {
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(units * C));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, (P)args...);
+}
+
 }  // namespace
 
 cudaError_t tq_launch_mass(const tq_params& p, const float* logits, int B, int Hq, int Hkv, int64_t T,
@@ -433,12 +519,12 @@ cudaError_t tq_launch_mass(const tq_params& p, const float* logits, int B, int H
   const int G = Hq / Hkv;
   const bool vec = T % 4 == 0;  // every row then starts on 16 bytes
   if (lse) {
-    const int64_t grid = units * ((T + (vec ? 1024 : 256) - 1) / (vec ? 1024 : 256));
+    const int64_t grid = units * ((T + kGivenKeys - 1) / kGivenKeys);
     if (grid > 0x7fffffffll) return cudaErrorNotSupported;
     if (vec)
-      mass_given_kernel<4><<<(unsigned)grid, 256, 0, st>>>(p, logits, Hq, Hkv, T, lens, lse, ex, decay, mass);
+      mass_given_kernel<true><<<(unsigned)grid, 256, 0, st>>>(p, logits, Hq, Hkv, T, lens, lse, ex, decay, mass);
     else
-      mass_given_kernel<1><<<(unsigned)grid, 256, 0, st>>>(p, logits, Hq, Hkv, T, lens, lse, ex, decay, mass);
+      mass_given_kernel<false><<<(unsigned)grid, 256, 0, st>>>(p, logits, Hq, Hkv, T, lens, lse, ex, decay, mass);
     return cudaGetLastError();
   }
   // blocks of a cluster: about two an SM over all units, at least 512 keys each,
@@ -448,20 +534,8 @@ cudaError_t tq_launch_mass(const tq_params& p, const float* logits, int B, int H
   while (C < 8 && ((units * C < 296 && T >= 1024 * C) || bytes(C) > kMassSmem)) C *= 2;
   if (units * C > 0x7fffffffll) return cudaErrorNotSupported;
   const size_t smem = bytes(C) <= kMassSmem ? bytes(C) : 0;
-  auto go = [&](auto fn) -> cudaError_t {
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMassSmem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {(unsigned)C, 1, 1};
-    cfg.gridDim = dim3((unsigned)(units * C));
-    cfg.blockDim = dim3(kMassThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, p, logits, Hq, Hkv, T, lens, ex, decay, mass);
+  auto go = [&](auto fn) {
+    return launch_cluster(fn, units, C, kMassThreads, smem, kMassSmem, st, p, logits, Hq, Hkv, T, lens, ex, decay, mass);
   };
   if (smem) return vec ? go(mass_kernel<4, true>) : go(mass_kernel<1, true>);
   return vec ? go(mass_kernel<4, false>) : go(mass_kernel<1, false>);
@@ -470,15 +544,18 @@ cudaError_t tq_launch_mass(const tq_params& p, const float* logits, int B, int H
 cudaError_t tq_launch_evict(const tq_params& p, const float* mass, int B, int Hkv, int64_t T, const int32_t* lens,
                             int64_t keep, int64_t sink, int64_t recent, int32_t* idx, float* mass_out,
                             int32_t* lens_out, cudaStream_t st) {
-  const unsigned grid = (unsigned)(B * Hkv);
-  if (T <= kEvKeep) {
-    const cudaError_t e = cudaFuncSetAttribute(evict_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvKeep * 4);
-    if (e != cudaSuccess) return e;
-    evict_kernel<true><<<grid, kEvThreads, (size_t)T * 4, st>>>(p, mass, Hkv, T, lens, keep, sink, recent, idx, mass_out, lens_out);
-  } else {
-    evict_kernel<false><<<grid, kEvThreads, 0, st>>>(p, mass, Hkv, T, lens, keep, sink, recent, idx, mass_out, lens_out);
-  }
-  return cudaGetLastError();
+  // blocks of a cluster: about two an SM over all units, at least 2048 keys
+  // each, and enough of them to keep the keys in shared memory where eight can
+  const int64_t units = (int64_t)B * Hkv;
+  auto part = [&](int64_t C) { return ((T + C - 1) / C + 31) & ~(int64_t)31; };
+  int C = 1;
+  while (C < 8 && ((units * C < 148 && part(2 * C) >= 2048) || part(C) > kEvKeep)) C *= 2;
+  if (units * C > 0x7fffffffll) return cudaErrorNotSupported;
+  if (part(C) <= kEvKeep)
+    return launch_cluster(evict_kernel<true>, units, C, kEvThreads, (size_t)part(C) * 4, kEvKeep * 4, st, p, mass, Hkv, T,
+                          lens, keep, sink, recent, idx, mass_out, lens_out);
+  return launch_cluster(evict_kernel<false>, units, C, kEvThreads, 0, 0, st, p, mass, Hkv, T, lens, keep, sink, recent,
+                        idx, mass_out, lens_out);
 }
 
 cudaError_t tq_launch_copy_rows(const tq_params& p, const tq_compressed& src, int64_t src_T, const tq_compressed& dst,
