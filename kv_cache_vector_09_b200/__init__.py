@@ -334,13 +334,14 @@ def _cache_arg(c: Optional[Compressed], name: str, codec: Codec, n: int):
     if c is None:
         assert n == 0, f"{name} is missing"
         return None
-    _arg(c.codes, name + ".codes", codec, torch.int32, n * codec.code_words)
-    _arg(c.norms, name + ".norms", codec, torch.float32, n)
+    codes = _arg(c.codes, "codes", codec, torch.int32, n * codec.code_words)
+    norms = _arg(c.norms, "norms", codec, torch.float32, n)
+    signs = rnorms = None
     if codec.m:
-        assert c.signs is not None and c.rnorms is not None, f"{name} lacks the codec's sketch"
-        _arg(c.signs, name + ".signs", codec, torch.int32, n * codec.sign_words)
-        _arg(c.rnorms, name + ".rnorms", codec, torch.float32, n)
-    return c.struct()
+        signs = _arg(c.signs, "signs", codec, torch.int32, n * codec.sign_words)
+        rnorms = _arg(c.rnorms, "rnorms", codec, torch.float32, n)
+        assert signs is not None and rnorms is not None, f"{name} lacks the codec's sketch"
+    return tq_compressed(codes, signs, norms, rnorms)
 
 
 def _ref(st):

@@ -114,6 +114,17 @@ __device__ __forceinline__ uint32_t peer_ld(const void* p, uint32_t rank) {
   return v;
 }
 
+__device__ __forceinline__ uint4 peer_ld4(const void* p, uint32_t rank) {
+  uint32_t a;
+  uint4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
 // No statistics given: a cluster of blocks takes one (sequence, KV head), each
 // an equal part of its keys, and each warp of a block one head's logits over a
 // piece of that part: it fetches them into shared memory (KEEP), leaves the
@@ -272,122 +283,130 @@ __device__ __forceinline__ int before_warp(const int* s, int warp, int lane) {
 }
 
 // A cluster of blocks: one (sequence, KV head), each block a contiguous part
-// of its keys.  A radix selection over the keys between the sinks and the
-// recent ones, eleven, eleven and ten bits, finds the smallest kept key and how
-// many of its equals stay (the lowest indices): every block counts its part's
-// digits and sums the counters of all.  Then every warp counts what stays in
-// its contiguous piece, and after one scan over warps and blocks writes it in
-// order.  The masses are read once and kept as ordered keys in shared memory
-// when they fit (KEEP).
+// of its keys.  Sinks and recent keys get the key 2^32 - 1, which no mass has,
+// so that the kept ones are the `keep` greatest of all.  A radix selection by
+// eleven, eleven and ten bits finds the smallest kept key and how many of its
+// equals stay (the lowest indices): every block counts its part's digits and
+// sums the counters of all.  Then every warp counts what stays in its
+// contiguous piece, and after one scan over warps and blocks writes it in order.
+// The masses are read once and kept as ordered keys in shared memory when they
+// fit (KEEP).  Bound by the instructions per key, hence the 16-byte reads.
 template <bool KEEP>
 __global__ void __launch_bounds__(kEvThreads)
     evict_kernel(const tq_params p, const float* __restrict__ mass, const int Hkv, const int64_t T,
                  const int32_t* __restrict__ lens, const int64_t keep, const int64_t sink, const int64_t recent,
                  int32_t* __restrict__ idx, float* __restrict__ mass_out, int32_t* __restrict__ lens_out) {
   extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ int s_hist[3][2048], s_sum[kEvWarps], s_sure[kEvWarps], s_equal[kEvWarps], s_total[2], s_need;
+  __shared__ __align__(16) int s_hist[3][2048];
+  __shared__ int s_sum[kEvWarps], s_sure[kEvWarps], s_equal[kEvWarps], s_total[2], s_need;
   __shared__ uint32_t s_key;
   const uint32_t rank = cluster_rank(), C = cluster_size();
   const int64_t bh = blockIdx.x / C;
   const int b = (int)(bh / Hkv), h = (int)(bh % Hkv);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t n = held_len(lens, b, T, p.err);
-  const float* mr = mass + bh * T;
+  const int n = (int)held_len(lens, b, T, p.err), room = (int)keep;
   int32_t* ir = idx + bh * keep;
   float* mo = mass_out ? mass_out + bh * keep : nullptr;
-  const int64_t kept = n < keep ? n : keep;
-  if (rank == 0 && h == 0 && tid == 0 && lens_out) lens_out[b] = (int32_t)kept;
-  for (int64_t i = kept + rank * kEvThreads + tid; i < keep; i += C * kEvThreads) {
+  const int kept = min(n, room);
+  if (rank == 0 && h == 0 && tid == 0 && lens_out) lens_out[b] = kept;
+  for (int64_t i = kept + (int64_t)(rank * kEvThreads + tid); i < room; i += C * kEvThreads) {
     ir[i] = -1;
     if (mo) mo[i] = 0.f;
   }
-  if (n <= keep) {  // for all blocks of the cluster alike
+  if (n <= room) {  // for all blocks of the cluster alike
     for (int64_t i = rank * kEvThreads + tid; i < n; i += C * kEvThreads) {
       ir[i] = (int32_t)i;
-      if (mo) mo[i] = mr[i];
+      if (mo) mo[i] = mass[bh * T + i];
     }
     return;
   }
-  const int64_t lo = sink, hi = n - recent;  // the keys to choose from: more than `need` of them
-  const int64_t part = ((n + C - 1) / C + 31) & ~(int64_t)31;
-  const int64_t p0 = min(n, rank * part), p1 = min(n, p0 + part);
+  // this block's keys: nk from key p0 on
+  const int64_t part = (((int64_t)n + C - 1) / C + 31) & ~(int64_t)31;
+  const int p0 = (int)min((int64_t)n, rank * part), nk = (int)min((int64_t)n - p0, part);
+  const float* mr = mass + bh * T + p0;
+  const int lo = (int)sink - p0, hi = n - (int)recent - p0;  // protected: below lo, from hi on
+  auto make_key = [&](int i) { return i < lo || i >= hi ? 0xffffffffu : mass_key(__ldg(mr + i)); };
   if (KEEP) {
 #pragma unroll 8
-    for (int64_t t = p0 + tid; t < p1; t += kEvThreads) keys[t - p0] = mass_key(__ldg(mr + t));
+    for (int i = tid; i < nk; i += kEvThreads) keys[i] = make_key(i);
+    if (tid < ((nk + 3) & ~3) - nk) keys[nk + tid] = 0u;  // the lowest key: the counters above it are right
   }
   for (int i = tid; i < 3 * 2048; i += kEvThreads) (&s_hist[0][0])[i] = 0;
-  auto key_of = [&](int64_t t) { return KEEP ? keys[t - p0] : mass_key(__ldg(mr + t)); };
-  int need = (int)(keep - sink - recent);
+  int need = room;
   uint32_t key = 0u;
-  const bool any = need > 0;
   __syncthreads();
-  if (any) {
-    const int64_t c0 = max(lo, p0), c1 = min(hi, p1);
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, digits = pass == 2 ? 1024 : 2048;
-      const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (pass == 1 ? 21 : 10);
-      int* hist = s_hist[pass];
-#pragma unroll 2
-      for (int64_t t0 = c0 + warp * 32; t0 < c1; t0 += kEvThreads) {
-        const int64_t t = t0 + lane;
-        const uint32_t k = t < c1 ? key_of(t) : 0u;
-        const bool in = t < c1 && (k & above) == key;
-        const int digit = (int)(k >> shift) & (digits - 1);
-        // lanes with the first lane's digit count as one: untouched keys, all
-        // of mass 0, would otherwise queue at a single counter
-        const uint32_t on = __ballot_sync(TQ_FULL_MASK, in);
-        if (on == 0u) continue;
-        const int lead = __shfl_sync(TQ_FULL_MASK, digit, __ffs(on) - 1);
-        const uint32_t same = __ballot_sync(TQ_FULL_MASK, in && digit == lead);
-        if (lane == __ffs(on) - 1) atomicAdd(&hist[lead], __popc(same));
-        if (in && digit != lead) atomicAdd(&hist[digit], 1);
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, digits = pass == 2 ? 1024 : 2048;
+    const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (pass == 1 ? 21 : 10);
+    int* hist = s_hist[pass];
+    int zeros = 0;  // keys of mass 0 (never looked at) would queue at one counter: counted apart
+    auto count = [&](uint32_t k) {
+      if ((k & above) == key) {
+        if (k == 0x80000000u)
+          ++zeros;
+        else
+          atomicAdd(&hist[(k >> shift) & (digits - 1)], 1);
       }
-      cluster_sync();
-      // the digit where the count from the top passes `need`: a thread sums
-      // digits / 512 counters from the top, then a scan over the block
-      const int each = digits / kEvThreads, top = digits - 1 - tid * each;
-      int c[4] = {0, 0, 0, 0}, x = 0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q < each) {
-          for (uint32_t r = 0; r < C; ++r) c[q] += (int)peer_ld(&hist[top - q], r);
-          x += c[q];
-        }
-      const int own = x;
-#pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {
-        const int y = __shfl_up_sync(TQ_FULL_MASK, x, s);
-        if (lane >= s) x += y;
+    };
+    if (KEEP) {
+      for (int i = 4 * tid; i < nk; i += 4 * kEvThreads) {
+        const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+        count(k.x);
+        count(k.y);
+        count(k.z);
+        count(k.w);
       }
-      if (lane == 31) s_sum[warp] = x;
-      __syncthreads();
-      int before = before_warp(s_sum, warp, lane) + x - own;  // greater digits than this thread's
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q < each) {
-          if (before < need && need <= before + c[q]) {
-            s_key = key | ((uint32_t)(top - q) << shift);
-            s_need = need - before;
-          }
-          before += c[q];
-        }
-      __syncthreads();
-      key = s_key;
-      need = s_need;
+    } else {
+      for (int i = tid; i < nk; i += kEvThreads) count(make_key(i));
     }
+    zeros = tq_warp_sum(zeros);
+    if (lane == 0 && zeros) atomicAdd(&hist[(0x80000000u >> shift) & (digits - 1)], zeros);
+    cluster_sync();
+    // the digit where the count from the top passes `need`: a thread sums four
+    // counters from the top (one 16-byte read a block), then a scan over the block
+    const int top = 2047 - 4 * tid;
+    int c[4] = {0, 0, 0, 0}, x = 0;
+    for (uint32_t r = 0; r < C; ++r) {
+      const uint4 y = peer_ld4(&hist[top - 3], r);
+      c[0] += (int)y.w;
+      c[1] += (int)y.z;
+      c[2] += (int)y.y;
+      c[3] += (int)y.x;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x += c[q];
+    const int own = x;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int y = __shfl_up_sync(TQ_FULL_MASK, x, s);
+      if (lane >= s) x += y;
+    }
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    int before = before_warp(s_sum, warp, lane) + x - own;  // greater digits than this thread's
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (before < need && need <= before + c[q]) {
+        s_key = key | ((uint32_t)(top - q) << shift);
+        s_need = need - before;
+      }
+      before += c[q];
+    }
+    __syncthreads();
+    key = s_key;
+    need = s_need;
   }
-  const int ties = any ? need : 0;  // of the keys equal to `key`
   // a warp's contiguous piece: what stays for certain, and how many equal `key`
-  const int64_t per = (((p1 - p0) + kEvWarps - 1) / kEvWarps + 31) & ~(int64_t)31;
-  const int64_t w0 = min(p1, p0 + warp * per), w1 = min(p1, w0 + per);
+  // (of which the first `need` stay)
+  const int per = ((nk + kEvWarps - 1) / kEvWarps + 31) & ~31;
+  const int w0 = min(nk, warp * per), w1 = min(nk, w0 + per);
   int sure = 0, equal = 0;
 #pragma unroll 4
-  for (int64_t t = w0 + lane; t < w1; t += 32) {
-    const bool mid = t >= lo && t < hi;
-    const uint32_t k = key_of(t);
-    sure += !mid || (any && k > key);
-    equal += mid && any && k == key;
+  for (int i = w0 + lane; i < w1; i += 32) {
+    const uint32_t k = KEEP ? keys[i] : make_key(i);
+    sure += k > key;
+    equal += k == key;
   }
   sure = tq_warp_sum(sure);
   equal = tq_warp_sum(equal);
@@ -409,20 +428,19 @@ __global__ void __launch_bounds__(kEvThreads)
     at += (int)peer_ld(&s_total[0], r);
     tied += (int)peer_ld(&s_total[1], r);
   }
-  cluster_sync();  // nobody leaves while its counters may be read
-  at += min(tied, ties);  // the equal ones that stay before this piece
-  for (int64_t t0 = w0; t0 < w1; t0 += 32) {
-    const int64_t t = t0 + lane;
-    const bool on = t < w1, mid = t >= lo && t < hi;
-    const uint32_t k = on ? key_of(t) : 0u;
-    const bool eq = on && mid && any && k == key;
-    const uint32_t be = __ballot_sync(TQ_FULL_MASK, eq), below = (1u << lane) - 1u;
-    const bool stay = on && (!mid || (any && (k > key || (eq && tied + __popc(be & below) < ties))));
+  cluster_sync();          // nobody leaves while its counters may be read
+  at += min(tied, need);   // the equal ones that stay before this piece
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < w1 ? (KEEP ? keys[i] : make_key(i)) : 0u, below = (1u << lane) - 1u;
+    const bool eq = i < w1 && k == key;
+    const uint32_t be = __ballot_sync(TQ_FULL_MASK, eq);
+    const bool stay = i < w1 && (k > key || (eq && tied + __popc(be & below) < need));
     const uint32_t bs = __ballot_sync(TQ_FULL_MASK, stay);
     if (stay) {
-      const int64_t o = at + __popc(bs & below);
-      ir[o] = (int32_t)t;
-      if (mo) mo[o] = __ldg(mr + t);
+      const int o = at + __popc(bs & below);
+      ir[o] = p0 + i;
+      if (mo) mo[o] = __ldg(mr + i);
     }
     at += __popc(bs);
     tied += __popc(be);
