@@ -147,8 +147,8 @@ template <int D, bool SPLIT>
 struct Layout {
   static constexpr int NP = SPLIT ? 2 : 1;              // fp16 parts of an operand
   static constexpr int kpart = kKeys * D * 2;           // one part of a key or value tile
-  static constexpr int VST = SPLIT ? 1 : 2;             // value stages
   int w, k, sg, v, total, kstage;
+  int vst;  // value stages: two where they fit (all but split d = 128 with m = 128)
   __host__ __device__ explicit Layout(int m) {
     w = 0;                                // W image: NP parts of [m / 8][128][16 bytes]
     const int wpart = kRows * m * 2;
@@ -156,7 +156,8 @@ struct Layout {
     sg = NP * kpart;                      // offset of the signs in a key stage
     kstage = sg + kKeys * m * 2;
     v = k + 2 * kstage;
-    total = v + VST * NP * kpart;
+    vst = v + 2 * NP * kpart <= 216 * 1024 ? 2 : 1;
+    total = v + vst * NP * kpart;
     const int rows_out = kRows * (D + 3) * 4;  // the block's result, over the same bytes
     if (total < rows_out) total = rows_out;
   }
@@ -735,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (nt > 0) load(cur);
     for (int j = 0; j < nt; ++j) {
-      const int sv = L::VST == 2 ? (j & 1) : 0, use = L::VST == 2 ? (j >> 1) : j;
+      const int sv = lay.vst == 2 ? (j & 1) : 0, use = lay.vst == 2 ? (j >> 1) : j;
       if (use >= 1) WAIT_WARP(sm.vempty[sv], (use & 1) ^ 1);
       unsigned char* st = dyn + lay.v + sv * L::NP * L::kpart;
 #pragma unroll 1
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (j > 0) {
           const int i0 = j - 1, s2 = i0 & 1, ph = (i0 >> 1) & 1;
-          const int sv = L::VST == 2 ? s2 : 0, use = L::VST == 2 ? (i0 >> 1) : i0;
+          const int sv = lay.vst == 2 ? s2 : 0, use = lay.vst == 2 ? (i0 >> 1) : i0;
           WAIT_WARP(sm.pfull[s2], ph);
           WAIT_WARP(sm.vfull[sv], use & 1);
           if (i0 >= 1) WAIT_WARP(sm.oempty, (i0 & 1) ^ 1);
