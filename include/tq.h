@@ -364,8 +364,10 @@ TQ_API tq_status tq_attend_prefix_workspace_size(const tq_codec *kc,
  *   lse      NULL, or [B][Hq] fp32: ln sum_t exp(scale * logit) over both
  *            parts, -inf without keys
  * The result of a call does not depend on other calls, and the same call gives
- * the same bits.  The logits, the exponentials' sums and the weighted values
- * are accumulated in fp32.  d <= 256, Hq / Hkv <= 32, a value sketch of m <= 128
+ * the same bits.  Logits, the exponentials' sums and the weighted values are
+ * accumulated in fp32, from operands good to 2^-22; with out_dtype TQ_BF16 and
+ * lse NULL from operands rounded once to fp16 (2^-11, an eighth of the
+ * result's own rounding).  d <= 256, Hq / Hkv <= 32, a value sketch of m <= 128
  * (else TQ_ERR_UNSUPPORTED).  workspace: 16-byte aligned; calls that may
  * overlap on the GPU need one each.                                          */
 TQ_API tq_status tq_attend_prefix(const tq_codec *kc, const tq_codec *vc,

@@ -197,6 +197,8 @@ BF, HF, FL = torch.bfloat16, torch.float16, torch.float32
     (64, dict(bits=(2,), m=64), dict(bits=(2,), seed=9), 3, 6, 2, 777, 129, [5, 129, 0], BF, BF),
     (64, dict(bits=(3,), m=128), dict(bits=(4,), seed=9), 33, 8, 2, 65, 64, [2 * i for i in range(33)], HF, HF),
     (64, dict(bits=(1, 2), m=32), dict(bits=(2, 3), seed=9), 2, 4, 4, 257, 31, [31, 30], BF, FL),
+    (128, dict(bits=(3,), m=96), V4, 2, 6, 3, 200, 70, [70, 1], HF, FL),                # three sign words
+    (64, dict(bits=(2,), m=32), dict(bits=(3,), seed=9), 300, 64, 2, 70, 5, [i % 6 for i in range(300)], BF, BF),  # more groups than SMs
     (256, dict(bits=(3,), m=64), dict(bits=(4,), seed=9), 2, 4, 2, 300, 70, [70, 0], BF, FL),
     (128, dict(bits=(2,), m=512), dict(bits=(2,), m=64, seed=9), 2, 4, 1, 200, 66, [0, 66], BF, FL),
     (128, K3, dict(bits=(3,), m=128, seed=9), 2, 4, 1, 200, 66, [0, 66], BF, BF),     # QJL-corrected values
@@ -293,6 +295,23 @@ def test_attend_prefix_on_another_stream_and_in_a_graph():
             assert torch.equal(want, got) and torch.equal(wl, gl)
         else:
             c.check(got, gl, c2)
+
+
+def test_attend_prefix_calls_that_overlap():
+    # two calls in flight on two streams, a workspace each, over the same caches
+    c = Case(128, K3, V4, 6, 8, 2, 3000, 90, [90, 0, 45, 89, 1, 64], seed=13)
+    (want, wl), (want16, _) = c.run(), c.run(BF, False)
+    torch.cuda.synchronize()
+    streams, ws = [torch.cuda.Stream() for _ in range(2)], [c.ws() for _ in range(2)]
+    outs = [torch.empty_like(want), torch.empty_like(want16)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                got.append(c.run(outs[k].dtype, k == 0, ws=ws[k], out=outs[k]))
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want16) and torch.equal(got[-2][1], wl)
 
 
 # ---------------------------------------------------------------------- mass
