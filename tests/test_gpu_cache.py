@@ -339,6 +339,7 @@ def mass_reference(logits, lens, lse, scale, decay, mass, Hkv):
     (3, 32, 8, 2048, None, True, 0.96875, 0.0),
     (1, 8, 2, 40003, [39999], False, 1.0, 0.0),
     (1, 32, 1, 131072, None, False, 1.0, 0.0),
+    (1, 32, 1, 60001, [60000], False, 1.0, 0.0),
     (1, 4, 1, 300001, [300000], True, 1.0, 0.0),
     (70, 4, 2, 333, [i * 333 // 69 for i in range(70)], False, 1.0, 0.0),
 ])
@@ -414,6 +415,7 @@ def evict_reference(mass, lens, keep, sink, recent):
     (1, 2, 20000, 19999, 0, 0, None, "equal"),
     (1, 2, 32768, 8192, 4, 1024, None, "ties"),
     (1, 1, 150001, 50000, 4, 100, [150000], "random"),
+    (1, 1, 420001, 3000, 4, 100, [420000], "ties"),
     (70, 2, 300, 64, 2, 8, [i * 300 // 69 for i in range(70)], "ties"),
 ])
 def test_evict_select(B, H, T, keep, sink, recent, lens, kind):
