@@ -365,11 +365,10 @@ TQ_API tq_status tq_attend_prefix_workspace_size(const tq_codec *kc,
  *            parts, -inf without keys
  * The result of a call does not depend on other calls, and the same call gives
  * the same bits.  Logits, the exponentials' sums and the weighted values are
- * accumulated in fp32, from operands good to 2^-22; with out_dtype TQ_BF16 and
- * lse NULL from operands rounded once to fp16 (2^-11, an eighth of the
- * result's own rounding).  d <= 256, Hq / Hkv <= 32, a value sketch of m <= 128
- * (else TQ_ERR_UNSUPPORTED).  workspace: 16-byte aligned; calls that may
- * overlap on the GPU need one each.                                          */
+ * accumulated in fp32, from operands good to 2^-22; out_dtype only rounds the
+ * result, and lse does not change it.  d <= 256, Hq / Hkv <= 32, a value sketch
+ * of m <= 128 (else TQ_ERR_UNSUPPORTED).  workspace: 16-byte aligned; calls that
+ * may overlap on the GPU need one each.                                      */
 TQ_API tq_status tq_attend_prefix(const tq_codec *kc, const tq_codec *vc,
                     const void *q, tq_dtype dtype, int B, int Hq, int Hkv,
                     float scale, int64_t Tp, const tq_compressed *Kp,

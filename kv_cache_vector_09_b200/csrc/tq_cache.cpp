@@ -159,8 +159,7 @@ extern "C" tq_status tq_attend_prefix(const tq_codec* kc, const tq_codec* vc, co
   if (lens && !aligned(lens, 4)) return tq_fail(TQ_ERR_INVALID_ARG, "%s: lens not 4-byte aligned", name);
   if (Tp > 0 && ((st = rows_ok(kc, Kp, name, "Kp")) != TQ_OK || (st = rows_ok(vc, Vp, name, "Vp")) != TQ_OK)) return st;
   if (T > 0 && ((st = rows_ok(kc, K, name, "K")) != TQ_OK || (st = rows_ok(vc, V, name, "V")) != TQ_OK)) return st;
-  tq_prefix_plan pl = plan_of(kc->p, vc->p, B, Hq, Hkv, Tp, T, sms_of(kc->device));
-  pl.split = out_dtype != TQ_BF16 || lse != nullptr;
+  const tq_prefix_plan pl = plan_of(kc->p, vc->p, B, Hq, Hkv, Tp, T, sms_of(kc->device));
   const size_t need = prefix_bytes(kc->p, vc->p, B, Hq, Hkv, pl);
   if (!aligned(workspace, 16) || ws_bytes < need)
     return tq_fail(TQ_ERR_INVALID_ARG, "%s: workspace null, misaligned or smaller than %zu bytes", name, need);

@@ -12,10 +12,9 @@ enum : uint32_t { kErrLength = 4, kErrRowIndex = 5 };
 // (sequence, KV head)'s own keys; each is cut into a fixed number of chunks,
 // and every (query row, chunk) leaves a partial (acc[d], max, sum[, a[m_v]]).
 struct tq_prefix_plan {
-  int nP;      // chunks per prefix unit (0: no prefix); tc: blocks per group of rows
-  int nO;      // chunks per own unit (0: no own keys, or tc)
-  bool tc;     // tensor-core kernel (tq_prefix_tc.cu)
-  bool split;  // its operands in two fp16 parts each
+  int nP;   // chunks per prefix unit (0: no prefix); tc: blocks per group of rows
+  int nO;   // chunks per own unit (0: no own keys, or tc)
+  bool tc;  // tensor-core kernel (tq_prefix_tc.cu)
 };
 
 struct tq_prefix_args {

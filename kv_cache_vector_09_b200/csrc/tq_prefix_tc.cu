@@ -20,11 +20,12 @@
 // norms; O starts from zero each tile, so that the tensor core's truncating
 // accumulation only ever spans one tile.
 //
-// SPLIT: operands as two fp16 parts each (x = hi + lo, 2^-22 relative) and the
-// three products that matter, hi hi + hi lo + lo hi, the small ones first.
-// Taken for fp32 and fp16 results and where the softmax's statistics are asked
-// for; a bf16 result (half a step 2^-8) comes from one product of fp16
-// operands (half a step 2^-11).
+// Operands are two fp16 parts each (x = hi + lo, 2^-22 relative) and a product
+// the three that matter, hi hi + hi lo + lo hi, the small ones first, whatever
+// the result's type: one part (2^-11) would move a logit by its size times
+// 2^-11, and a weight by e to that, which at logits of 100 is twice a bf16
+// result's half step (32 sequences over 32,768 keys: 0.119 ms with one part,
+// 0.135 with two).
 //
 // Operand bytes come from byte permutes: a code of up to three bits is a prmt
 // selector into the eight low or high bytes of the codebook's fp16 values; the
@@ -40,10 +41,10 @@
 // unrolling stay loops: all unrolled, a tile took up to 6300 cycles.
 //
 // Measured (B200, d = 128, 8 KV heads, 32 query heads, 3-bit keys with m = 128,
-// 4-bit values): 32 sequences over 32,768 + up to 1024 keys, bf16, 0.120 ms (220
+// 4-bit values): 32 sequences over 32,768 + up to 1024 keys, bf16, 0.135 ms (196
 // TFLOP/s); 64 over 16,411 + up to 777, fp32 with statistics, 0.168 ms.  Bound by
-// the latency of one tile's chain through its warps, about 3000 cycles (3500
-// split) for 900 (2300) of tensor-core time; reading the records is 9 us of it.
+// the latency of one tile's chain through its warps, about 3500 cycles for 2300 of
+// tensor-core time; reading the records is 9 us of it.
 #include <math.h>
 
 #include <algorithm>
@@ -150,12 +151,12 @@ struct Smem {
   int64_t len[kRows];                                        // keys of the block's sequences
 };
 
-template <int D, bool SPLIT>
+template <int D>
 struct Layout {
-  static constexpr int NP = SPLIT ? 2 : 1;              // fp16 parts of an operand
+  static constexpr int NP = 2;                          // fp16 parts of an operand
   static constexpr int kpart = kKeys * D * 2;           // one part of a key or value tile
   int w, k, sg, v, total, kstage;
-  int vst;  // value stages: two where they fit (all but split d = 128 with m = 128)
+  int vst;  // value stages: two where they fit (all but d = 128 with m = 128)
   __host__ __device__ explicit Layout(int m) {
     w = 0;                                // W image: NP parts of [m / 8][128][16 bytes]
     const int wpart = kRows * m * 2;
@@ -171,8 +172,8 @@ struct Layout {
 };
 
 // 32 coordinates of one key from their bit planes: 4 chunks of 16 bytes at
-// `dst` + 1024 s (and the low parts at dst + lo_off)
-template <int P, bool SPLIT>
+// `dst` + 1024 s, and the low parts at dst + lo_off
+template <int P>
 __device__ __forceinline__ void expand32(const uint32_t (&pl)[4], const Tab& t, unsigned char* dst, int lo_off) {
   const uint32_t neg = ~pl[3];  // P = 4: the top bit is the sign, the others the magnitude or its complement
   uint32_t w[3];
@@ -197,25 +198,21 @@ __device__ __forceinline__ void expand32(const uint32_t (&pl)[4], const Tab& t, 
       const uint32_t a = prmt(t.hl[0], t.hl[1], sl), b = prmt(t.hh[0], t.hh[1], sl) ^ sg;
       ph[2 * h] = prmt(a, b, 0x5140);
       ph[2 * h + 1] = prmt(a, b, 0x7362);
-      if constexpr (SPLIT) {
-        const uint32_t c = prmt(t.ll[0], t.ll[1], sl), e = prmt(t.lh[0], t.lh[1], sl) ^ sg;
-        pw[2 * h] = prmt(c, e, 0x5140);
-        pw[2 * h + 1] = prmt(c, e, 0x7362);
-      }
+      const uint32_t c = prmt(t.ll[0], t.ll[1], sl), e = prmt(t.lh[0], t.lh[1], sl) ^ sg;
+      pw[2 * h] = prmt(c, e, 0x5140);
+      pw[2 * h + 1] = prmt(c, e, 0x7362);
     }
     *reinterpret_cast<uint4*>(dst + 1024 * s) = hi;
-    if constexpr (SPLIT) *reinterpret_cast<uint4*>(dst + 1024 * s + lo_off) = lo;
+    *reinterpret_cast<uint4*>(dst + 1024 * s + lo_off) = lo;
   }
 }
 
-template <bool SPLIT>
-__device__ __forceinline__ void expand_group(int bits, const uint32_t (&pl)[4], const Tab& t, unsigned char* dst,
-                                             int lo_off) {
+__device__ __forceinline__ void expand_group(int bits, const uint32_t (&pl)[4], const Tab& t, unsigned char* dst, int lo_off) {
   switch (bits) {
-    case 1: expand32<1, SPLIT>(pl, t, dst, lo_off); break;
-    case 2: expand32<2, SPLIT>(pl, t, dst, lo_off); break;
-    case 3: expand32<3, SPLIT>(pl, t, dst, lo_off); break;
-    default: expand32<4, SPLIT>(pl, t, dst, lo_off);
+    case 1: expand32<1>(pl, t, dst, lo_off); break;
+    case 2: expand32<2>(pl, t, dst, lo_off); break;
+    case 3: expand32<3>(pl, t, dst, lo_off); break;
+    default: expand32<4>(pl, t, dst, lo_off);
   }
 }
 
@@ -379,10 +376,10 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <int D, bool SPLIT, bool SK>
+template <int D, bool SK>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const tq_params kp, const tq_params vp, const tq_prefix_args A, const int nC, const int SB) {
-  using L = Layout<D, SPLIT>;
+  using L = Layout<D>;
   constexpr int NWH = D / 64;
   extern __shared__ __align__(1024) unsigned char dyn[];
   __shared__ Smem sm;
@@ -566,20 +563,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               const u64 p = pair(__float_as_uint(ex2(e.x)), __float_as_uint(ex2(e.y)));
               z = add2(z, p);
               const u64 pv = mul2(p, w ? v2.y : v2.x);
-              if (SPLIT) {
-                // high part: the leading 11 bits; the rest is exact in fp32
-                const u64 top = pv & 0xffffe000ffffe000ull;
-                const float2 g = parts(top), q = parts(fma2(top, pair(-1.f), pv));
-                hi[i + w] = pack_f16(g.x, g.y);
-                lo[i + w] = pack_f16(q.x, q.y);
-              } else {
-                const float2 f = parts(pv);
-                hi[i + w] = pack_f16(f.x, f.y);
-              }
+              // high part: the leading 11 bits; the rest is exact in fp32
+              const u64 top = pv & 0xffffe000ffffe000ull;
+              const float2 g = parts(top), q = parts(fma2(top, pair(-1.f), pv));
+              hi[i + w] = pack_f16(g.x, g.y);
+              lo[i + w] = pack_f16(q.x, q.y);
             }
           }
           tqtc::tmem_st8(s_col + k0 / 2, hi);
-          if (SPLIT) tqtc::tmem_st8(s_col + 64 + k0 / 2, lo);
+          tqtc::tmem_st8(s_col + 64 + k0 / 2, lo);
         }
         tqtc::tmem_wait_st();
         if (act) {
@@ -692,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < NWH; ++i) {
         const uint32_t pl[4] = {kw[0][0], kw[1][0], kw[2][0], kw[3][0]};
-        expand_group<SPLIT>(kbits, pl, tk, st + (half * NWH + i) * 4096 + off, L::kpart);
+        expand_group(kbits, pl, tk, st + (half * NWH + i) * 4096 + off, L::kpart);
 #pragma unroll
         for (int p = 0; p < 4; ++p) kw[p][0] = kw[p][NWH - 1];
       }
@@ -750,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < NWH; ++i) {
         const uint32_t pl[4] = {vw[0][0], vw[1][0], vw[2][0], vw[3][0]};
-        expand_group<SPLIT>(vbits, pl, tv, st + (half * NWH + i) * 4096 + off, L::kpart);
+        expand_group(vbits, pl, tv, st + (half * NWH + i) * 4096 + off, L::kpart);
 #pragma unroll
         for (int p = 0; p < 4; ++p) vw[p][0] = vw[p][NWH - 1];
       }
@@ -783,21 +775,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t dS = tu + 128 * s2, kst = base + lay.k + s2 * lay.kstage;
             // parts: low queries, low keys, then the high product
 #pragma unroll 1
-            for (int pr = SPLIT ? 0 : 2; pr < 3; ++pr) {
+            for (int pr = 0; pr < 3; ++pr) {
               const uint32_t qa = tu + kColQ + (pr == 0 ? D / 2 : 0);
               const uint64_t kd = tqtc::smem_desc(kst + (pr == 1 ? L::kpart : 0), 1024, 128);
 #pragma unroll
               for (int k = 0; k < D / 16; ++k)
-                tqtc::mma_f16_ts(dS, qa + 8 * k, kd + 128 * k, idS, !(k == 0 && pr == (SPLIT ? 0 : 2)));
+                tqtc::mma_f16_ts(dS, qa + 8 * k, kd + 128 * k, idS, !(k == 0 && pr == 0));
             }
             if (SK) {
               const uint64_t sd = tqtc::smem_desc(kst + lay.sg, 1024, 128);
 #pragma unroll 1
-              for (int pr = SPLIT ? 0 : 1; pr < 2; ++pr) {
+              for (int pr = 0; pr < 2; ++pr) {
                 const uint64_t wd = tqtc::smem_desc(base + lay.w + (pr == 0 ? kRows * kp.m * 2 : 0), 2048, 128);
 #pragma unroll 1
                 for (int k = 0; k < ks; ++k) {
-                  tqtc::mma_f16_ss(dS + 64, wd + 512 * k, sd + 256 * k, idS, !(k == 0 && pr == (SPLIT ? 0 : 1)));
+                  tqtc::mma_f16_ss(dS + 64, wd + 512 * k, sd + 256 * k, idS, !(k == 0 && pr == 0));
                   tqtc::mma_f16_ss(dS + 64, wd + 512 * k + 256, sd + 256 * k + 128, idS, true);
                 }
               }
@@ -817,12 +809,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect()) {
             const uint32_t dO = tu + kColO, pA = tu + 128 * s2, vst = base + lay.v + sv * L::NP * L::kpart;
 #pragma unroll 1
-            for (int pr = SPLIT ? 0 : 2; pr < 3; ++pr) {
+            for (int pr = 0; pr < 3; ++pr) {
               const uint32_t pa = pA + (pr == 0 ? 64 : 0);
               const uint64_t vd = tqtc::smem_desc(vst + (pr == 1 ? L::kpart : 0), 128, 1024);
 #pragma unroll
               for (int k = 0; k < kKeys / 16; ++k)
-                tqtc::mma_f16_ts(dO, pa + 32 * (k >> 1) + 8 * (k & 1), vd + 16 * k, idO, !(k == 0 && pr == (SPLIT ? 0 : 2)));
+                tqtc::mma_f16_ts(dO, pa + 32 * (k >> 1) + 8 * (k & 1), vd + 16 * k, idO, !(k == 0 && pr == 0));
             }
             tqtc::mma_commit(&sm.vempty[sv]);
             tqtc::mma_commit(&sm.ofull);
@@ -864,11 +856,11 @@ cudaError_t launch_prep(const tq_params& kp, const tq_prefix_args& a, int SB, un
   return cudaGetLastError();
 }
 
-template <int D, bool SPLIT, bool SK>
+template <int D, bool SK>
 cudaError_t launch(const tq_params& kp, const tq_params& vp, const tq_prefix_args& a, int nC, int SB, unsigned groups,
                    cudaStream_t st) {
-  const Layout<D, SPLIT> lay(kp.m);
-  auto fn = prefix_tc_kernel<D, SPLIT, SK>;
+  const Layout<D> lay(kp.m);
+  auto fn = prefix_tc_kernel<D, SK>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, lay.total);
   if (e != cudaSuccess) return e;
   e = a.dtype == TQ_F32    ? launch_prep<D, float>(kp, a, SB, groups, st)
@@ -911,13 +903,7 @@ cudaError_t tq_launch_prefix_tc(const tq_params& kp, const tq_params& vp, const 
   const int64_t groups = groups_of(a.B, a.Hkv, a.G);
   if (groups * std::max(plan.nP, kRows / kPrepRows) > 0x7fffffffll) return cudaErrorNotSupported;
   const unsigned g = (unsigned)groups;
-#define GO(DD, SS) \
-  return kp.m ? launch<DD, SS, true>(kp, vp, a, plan.nP, SB, g, st) : launch<DD, SS, false>(kp, vp, a, plan.nP, SB, g, st)
-  if (kp.d == 64) {
-    if (plan.split) GO(64, true);
-    GO(64, false);
-  }
-  if (plan.split) GO(128, true);
-  GO(128, false);
-#undef GO
+  if (kp.d == 64)
+    return kp.m ? launch<64, true>(kp, vp, a, plan.nP, SB, g, st) : launch<64, false>(kp, vp, a, plan.nP, SB, g, st);
+  return kp.m ? launch<128, true>(kp, vp, a, plan.nP, SB, g, st) : launch<128, false>(kp, vp, a, plan.nP, SB, g, st);
 }
