@@ -1,113 +1,16 @@
-"""Shared-prefix attention and bounded cache at the edges of their contract:
-calls from several host threads, weights with infinite statistics and logits or
-without a history, and the weights' way through eviction."""
-import ctypes
+"""The bounded cache at the edges of its contract."""
 import math
-import threading
 
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_cache import DEV, Case, evict_reference
+from test_gpu_cache import DEV, evict_reference
 
 pytestmark = pytest.mark.gpu
 
 tq = pytest.importorskip("kv_cache_vector_09_b200")
 U = 2.0 ** -24
-
-
-# ------------------------------------------------------- several host threads
-def test_calls_from_two_host_threads():
-    # codecs of one kernel that need different amounts of shared memory: a call
-    # must not depend on what another thread launches between its own steps
-    V, VG = dict(bits=(4,), seed=4), dict(bits=(4,), seed=9)
-    pairs = [[Case(128, dict(bits=(3,), m=m), V, 2, 8, 2, 200, 20, [20, 3], seed=m) for m in (128, 0)],
-             [Case(256, dict(bits=(3,), m=m), VG, 2, 4, 2, 70, 20, [20, 3], seed=m) for m in (1024, 32)]]
-    for cases in pairs:
-        want = [c.run()[0] for c in cases]
-        torch.cuda.synchronize()
-        failed, go = [], threading.Barrier(2)
-
-        def work(c, w):
-            # the C entry itself, its arguments made beforehand: calls overlap outside the interpreter's lock
-            torch.cuda.set_device(0)
-            st, ws, out, g = torch.cuda.Stream(), c.ws(), torch.empty_like(w), c.g
-            rec = [g[k].struct() for k in ("Kp", "Vp", "K", "V")]
-            Kp, Vp, K, V = (ctypes.byref(r) for r in rec)
-            args = (c.kc.handle, c.vc.handle, g["q"].data_ptr(), tq.TQ_BF16, c.B, c.Hq, c.Hkv, c.scale, c.Tp, Kp, Vp, c.T,
-                    g["lens"].data_ptr(), K, V, ws.data_ptr(), ws.numel() * ws.element_size(), out.data_ptr(), tq.TQ_F32,
-                    None, st.cuda_stream)
-            call = tq.c_api().tq_attend_prefix
-            torch.cuda.synchronize()
-            go.wait()
-            bad = sum(call(*args) != 0 for _ in range(20000))
-            st.synchronize()
-            if bad or not torch.equal(out, w):
-                failed.append((c.okc.m, bad, tq.tq_last_error_string()))
-
-        threads = [threading.Thread(target=work, args=x) for x in zip(cases, want)]
-        [t.start() for t in threads]
-        [t.join() for t in threads]
-        assert not failed, failed
-
-
-# --------------------------------------------------------------------- weights
-#         B, Hq, Hkv, T, lens, statistics given
-WEIGHTS = [(2, 4, 2, 7, [7, 3], False), (2, 8, 2, 3000, None, False), (1, 8, 2, 4001, [4000], False),
-           (1, 32, 1, 60001, [60000], False), (1, 32, 1, 65536, None, False),
-           (2, 8, 2, 3000, [3000, 1], True), (2, 5, 5, 4097, None, True)]
-
-
-def weights(B, Hq, Hkv, T, lens, with_lse, mass, decay, logits=None, lse=None, scale=0.0):
-    g = torch.Generator(device=DEV)
-    g.manual_seed(T)
-    kc = tq.Codec(128, (3,), 0, 0)
-    if logits is None:
-        logits = torch.randn((B, Hq, T), generator=g, device=DEV) * 20.0
-    if with_lse and lse is None:
-        lse = torch.logsumexp(logits.double() / math.sqrt(128), -1).float()
-    n = None if lens is None else torch.tensor(lens, dtype=torch.int32, device=DEV)
-    tq.tq_mass_update(kc, logits, B, Hq, Hkv, T, mass, lens=n, lse=lse, scale=scale, decay=decay)
-    return mass
-
-
-@pytest.mark.parametrize("B,Hq,Hkv,T,lens,with_lse", WEIGHTS)
-def test_a_decay_of_zero_forgets_the_old_weight(B, Hq, Hkv, T, lens, with_lse):
-    # whatever the buffer holds, NaN and infinities included
-    want = weights(B, Hq, Hkv, T, lens, with_lse, torch.zeros((B, Hkv, T), device=DEV), 1.0)
-    for old in (math.nan, math.inf, 3.0):
-        got = weights(B, Hq, Hkv, T, lens, with_lse, torch.full((B, Hkv, T), old, device=DEV), 0.0)
-        for b in range(B):
-            n = T if lens is None else lens[b]
-            assert torch.equal(got[b, :, :n], want[b, :, :n]) and torch.isfinite(got[b, :, :n]).all()
-            assert torch.equal(got[b, :, n:].isnan(), torch.full_like(got[b, :, n:], old).isnan())  # left alone
-
-
-@pytest.mark.parametrize("T", [8, 4097])
-def test_a_statistic_of_infinity_adds_nothing(T):
-    # e^(l - inf) = 0, as for a row without keys
-    lse = torch.tensor([[math.inf, -math.inf, 9.0, math.inf]], device=DEV)
-    logits = torch.randn((1, 4, T), generator=torch.Generator().manual_seed(T)).to(DEV) * 20.0
-    got = weights(1, 4, 2, T, None, True, torch.ones((1, 2, T), device=DEV), 0.5, logits, lse)
-    assert torch.all(got[0, 0] == 0.5)
-    p = torch.exp(logits[0, 2].double() / math.sqrt(128) - 9.0)
-    assert torch.all((got[0, 1].double() - 0.5 - p).abs() <= U * (1 + 40 * p))  # |exponent| <= 20: 20 u, exp2 4 u
-
-
-@pytest.mark.parametrize("T", [8, 4097])
-def test_infinite_logits_follow_the_definition(T):
-    # e^(-inf) = 0 at every scale, and e^(inf) = inf
-    lse = torch.zeros((1, 2), device=DEV)
-    for scale in (1e-38, 0.5, 64.0):
-        logits = torch.zeros((1, 2, T), device=DEV)
-        logits[0, :, 0::3] = -math.inf
-        logits[0, 0, 1] = math.inf
-        got = weights(1, 2, 2, T, None, True, torch.ones((1, 2, T), device=DEV), 1.0, logits, lse, scale)
-        want = torch.full((2, T), 2.0, device=DEV)
-        want[:, 0::3] = 1.0
-        want[0, 1] = math.inf
-        assert torch.equal(got[0], want), scale
 
 
 def test_weights_follow_their_keys_through_eviction():
