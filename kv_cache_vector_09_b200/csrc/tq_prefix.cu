@@ -24,6 +24,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kNG = 8;           // query rows of a block
+// most dynamic shared memory of a block: d <= 256, m <= 1024, chunks of <= 1024
+// keys.  The limit is set to it, the same for every call: the attribute is the
+// process's, and one thread's launch may come between another's two steps
+constexpr int kMostSmem = (int)sizeof(float) * kNG * (256 + 1024 + 1024);
 
 // length of sequence b's own context, clamped to [0, T]; an entry outside is
 // recorded in the codec's error word
@@ -375,7 +379,8 @@ cudaError_t tq_launch_prefix_any(const tq_params& kp, const tq_params& vp, const
   if (plan.nP) per = std::max<int64_t>(per, (a.Tp + plan.nP - 1) / plan.nP);
   if (plan.nO) per = std::max<int64_t>(per, (a.T + plan.nO - 1) / plan.nO);
   const size_t smem = sizeof(float) * (size_t)kNG * (kp.d + kp.m + per);
-  cudaError_t e = cudaFuncSetAttribute(prefix_any_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > (size_t)kMostSmem) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = cudaFuncSetAttribute(prefix_any_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
   if (e != cudaSuccess) return e;
   prefix_any_kernel<<<(unsigned)grid, kThreads, smem, st>>>(kp, vp, a, plan.nP, plan.nO, subP, subO);
   return cudaGetLastError();

@@ -58,6 +58,10 @@ namespace {
 constexpr int kKeys = 64;    // keys of a tile
 constexpr int kRows = 128;   // rows of a block
 constexpr int kThreads = 896;
+// largest key sketch.  Limits of shared memory are set for it, the same for
+// every call: the attribute is the process's, and one thread's launch may come
+// between another's two steps
+constexpr int kMostM = 128;
 constexpr int kAccWarp0 = 8, kKeyWarp0 = 16, kValWarp0 = 20, kMmaWarp = 24;
 // registers a thread after the roles have split the 72 of the launch:
 // 2 * 80 + 2 * 88 + 72 + 72 + 24 = 7 * 72
@@ -850,7 +854,7 @@ template <int D, typename TIn>
 cudaError_t launch_prep(const tq_params& kp, const tq_prefix_args& a, int SB, unsigned groups, cudaStream_t st) {
   auto fn = prefix_prep_kernel<D, TIn>;
   const size_t smem = sizeof(float) * (size_t)D * kp.m;
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(float) * D * kMostM);
   if (e != cudaSuccess) return e;
   fn<<<groups * (kRows / kPrepRows), 256, smem, st>>>(kp, (const TIn*)a.q, a.B, a.Hq, a.G, SB, a.image, a.scales);
   return cudaGetLastError();
@@ -861,7 +865,9 @@ cudaError_t launch(const tq_params& kp, const tq_params& vp, const tq_prefix_arg
                    cudaStream_t st) {
   const Layout<D> lay(kp.m);
   auto fn = prefix_tc_kernel<D, SK>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, lay.total);
+  int most = 0;  // m = 96 needs more than m = 128, which has one value stage
+  for (int m = 0; m <= kMostM; m += 32) most = std::max(most, Layout<D>(m).total);
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   e = a.dtype == TQ_F32    ? launch_prep<D, float>(kp, a, SB, groups, st)
       : a.dtype == TQ_BF16 ? launch_prep<D, __nv_bfloat16>(kp, a, SB, groups, st)
@@ -885,7 +891,7 @@ cudaError_t launch(const tq_params& kp, const tq_params& vp, const tq_prefix_arg
 }  // namespace
 
 bool tq_prefix_tc_supported(const tq_params& kp, const tq_params& vp) {
-  return (kp.d == 64 || kp.d == 128) && kp.m <= 128 && vp.m == 0 && !kp.vq_bits && !vp.vq_bits;
+  return (kp.d == 64 || kp.d == 128) && kp.m <= kMostM && vp.m == 0 && !kp.vq_bits && !vp.vq_bits;
 }
 
 static int64_t groups_of(int B, int Hkv, int G) { return (int64_t)Hkv * ((B + kRows / G - 1) / (kRows / G)); }

@@ -1,11 +1,13 @@
-"""The bounded cache at the edges of its contract."""
+"""Shared-prefix attention and bounded cache at the edges of their contract."""
+import ctypes
 import math
+import threading
 
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_cache import DEV, evict_reference
+from test_gpu_cache import DEV, Case, evict_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -13,6 +15,42 @@ tq = pytest.importorskip("kv_cache_vector_09_b200")
 U = 2.0 ** -24
 
 
+# ------------------------------------------------------- several host threads
+def test_calls_from_two_host_threads():
+    # codecs of one kernel that need different amounts of shared memory: a call
+    # must not depend on what another thread launches between its own steps
+    V, VG = dict(bits=(4,), seed=4), dict(bits=(4,), seed=9)
+    pairs = [[Case(128, dict(bits=(3,), m=m), V, 2, 8, 2, 200, 20, [20, 3], seed=m) for m in ms] for ms in ((128, 0), (96, 32))]
+    pairs += [[Case(256, dict(bits=(3,), m=m), VG, 2, 4, 2, 70, 20, [20, 3], seed=m) for m in (1024, 32)]]
+    for cases in pairs:
+        want = [c.run()[0] for c in cases]
+        torch.cuda.synchronize()
+        failed, go = [], threading.Barrier(2)
+
+        def work(c, w):
+            # the C entry itself, its arguments made beforehand: calls overlap outside the interpreter's lock
+            torch.cuda.set_device(0)
+            st, ws, out, g = torch.cuda.Stream(), c.ws(), torch.empty_like(w), c.g
+            rec = [g[k].struct() for k in ("Kp", "Vp", "K", "V")]
+            Kp, Vp, K, V = (ctypes.byref(r) for r in rec)
+            args = (c.kc.handle, c.vc.handle, g["q"].data_ptr(), tq.TQ_BF16, c.B, c.Hq, c.Hkv, c.scale, c.Tp, Kp, Vp, c.T,
+                    g["lens"].data_ptr(), K, V, ws.data_ptr(), ws.numel() * ws.element_size(), out.data_ptr(), tq.TQ_F32,
+                    None, st.cuda_stream)
+            call = tq.c_api().tq_attend_prefix
+            torch.cuda.synchronize()
+            go.wait()
+            bad = sum(call(*args) != 0 for _ in range(20000))
+            st.synchronize()
+            if bad or not torch.equal(out, w):
+                failed.append((c.okc.m, bad, tq.tq_last_error_string()))
+
+        threads = [threading.Thread(target=work, args=x) for x in zip(cases, want)]
+        [t.start() for t in threads]
+        [t.join() for t in threads]
+        assert not failed, failed
+
+
+# --------------------------------------------------------------------- weights
 def test_weights_follow_their_keys_through_eviction():
     """Steps of a bounded cache: the accumulated weight of every key against the
     64-bit sum over that key's own logits and statistics, where it started and
