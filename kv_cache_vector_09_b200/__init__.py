@@ -367,7 +367,7 @@ def tq_attend_prefix(kc: Codec, vc: Codec, q: torch.Tensor, B: int, Hq: int, Hkv
     ko, vo = _cache_arg(K, "K", kc, B * Hkv * T), _cache_arg(V, "V", vc, B * Hkv * T)
     _check(_lib.tq_attend_prefix(kc.handle, vc.handle, _arg(q, "q", kc, q.dtype, B * Hq * kc.d), _DTYPES[q.dtype], B,
                                  Hq, Hkv, scale, Tp, _ref(ks), _ref(vs), T, _arg(lens, "lens", kc, torch.int32, B),
-                                 _ref(ko), _ref(vo), workspace.data_ptr(),
+                                 _ref(ko), _ref(vo), _arg(workspace, "workspace", kc, workspace.dtype, 0),
                                  workspace.numel() * workspace.element_size(),
                                  _arg(out, "out", kc, out.dtype, B * Hq * kc.d), _DTYPES[out.dtype],
                                  _arg(lse, "lse", kc, torch.float32, B * Hq), _stream(stream)), "tq_attend_prefix")
