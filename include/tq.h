@@ -390,7 +390,8 @@ TQ_API tq_status tq_attend_prefix(const tq_codec *kc, const tq_codec *vc,
  *            -inf adds nothing.  NULL: the softmax over the row's own lens[b]
  *            keys; a row whose logits are all -inf adds nothing
  *   scale    0 -> 1/sqrt(d) of kc
- *   decay    finite; 1 keeps the sum, less than 1 lets old weight fade
+ *   decay    finite; 1 keeps the sum, less than 1 lets old weight fade, 0 starts
+ *            anew: the old content of mass is then not read
  *   mass     [B][Hkv][T] fp32, updated in place; entries at t >= lens[b] are
  *            left as they were
  * Hq / Hkv <= 32.                                                            */

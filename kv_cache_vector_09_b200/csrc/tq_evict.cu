@@ -26,7 +26,8 @@ __device__ __forceinline__ int64_t held_len(const int32_t* lens, int b, int64_t 
 }
 
 // ---------------------------------------------------------------- mass
-// mass_t <- decay mass_t + sum_g e^(scale l_gt - lse_g), t < len.  The exponent
+// mass_t <- decay mass_t + sum_g e^(scale l_gt - lse_g), t < len; a decay of 0
+// does not read the old weight, which may be anything.  The exponent
 // is taken in base 2 with c = scale log2(e) in two parts (ch + cl), so that
 // the product's rounding does not grow with |l|.
 struct Exponent {
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(256)
   const int left = (int)min((int64_t)kGivenKeys, n - t0), tid = threadIdx.x;
   float add[4] = {0.f, 0.f, 0.f, 0.f};
   if (VEC && 4 * tid + 4 <= left) {
-    const float4 m = *reinterpret_cast<const float4*>(mr + 4 * tid);
+    const float4 m = decay != 0.f ? *reinterpret_cast<const float4*>(mr + 4 * tid) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int g = 0; g < G; ++g) {
       const float4 l = __ldg(reinterpret_cast<const float4*>(lg + g * T) + tid);
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(256)
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (first + i * step < left) mr[first + i * step] = fmaf(mr[first + i * step], decay, add[i]);
+    if (first + i * step < left) mr[first + i * step] = decay != 0.f ? fmaf(mr[first + i * step], decay, add[i]) : add[i];
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kMassThreads)
     for (int i = 0; i < V; ++i) add[i] = 0.f;
     const int sub = KEEP ? k / ps : 0;  // ps % 4 = 0: the V keys are of one piece
     if (V == 4 && k + 4 <= len) {
-      float4 m = *reinterpret_cast<const float4*>(mr + k);
+      float4 m = decay != 0.f ? *reinterpret_cast<const float4*>(mr + k) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int g = 0; g < G; ++g) {
         float4 e;
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kMassThreads)
           else
             a = fmaf(ex2((__ldg(lg + g * T + q) - s_M[g]) * ex.ch), s_rz[g], a);
         }
-        mr[q] = fmaf(mr[q], decay, a);
+        mr[q] = decay != 0.f ? fmaf(mr[q], decay, a) : a;
       }
     }
   }

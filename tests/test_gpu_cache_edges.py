@@ -1,4 +1,6 @@
-"""Shared-prefix attention and bounded cache at the edges of their contract."""
+"""Shared-prefix attention and bounded cache at the edges of their contract:
+calls from several host threads, weights without a history or with infinite
+statistics and logits, and the weights' way through eviction."""
 import ctypes
 import math
 import threading
@@ -51,6 +53,37 @@ def test_calls_from_two_host_threads():
 
 
 # --------------------------------------------------------------------- weights
+#         B, Hq, Hkv, T, lens, statistics given
+WEIGHTS = [(2, 4, 2, 7, [7, 3], False), (2, 8, 2, 3000, None, False), (1, 8, 2, 4001, [4000], False),
+           (1, 32, 1, 60001, [60000], False), (1, 32, 1, 65536, None, False),
+           (2, 8, 2, 3000, [3000, 1], True), (2, 5, 5, 4097, None, True)]
+
+
+def weights(B, Hq, Hkv, T, lens, with_lse, mass, decay, logits=None, lse=None, scale=0.0):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    kc = tq.Codec(128, (3,), 0, 0)
+    if logits is None:
+        logits = torch.randn((B, Hq, T), generator=g, device=DEV) * 20.0
+    if with_lse and lse is None:
+        lse = torch.logsumexp(logits.double() / math.sqrt(128), -1).float()
+    n = None if lens is None else torch.tensor(lens, dtype=torch.int32, device=DEV)
+    tq.tq_mass_update(kc, logits, B, Hq, Hkv, T, mass, lens=n, lse=lse, scale=scale, decay=decay)
+    return mass
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,T,lens,with_lse", WEIGHTS)
+def test_a_decay_of_zero_forgets_the_old_weight(B, Hq, Hkv, T, lens, with_lse):
+    # whatever the buffer holds, NaN and infinities included
+    want = weights(B, Hq, Hkv, T, lens, with_lse, torch.zeros((B, Hkv, T), device=DEV), 1.0)
+    for old in (math.nan, math.inf, 3.0):
+        got = weights(B, Hq, Hkv, T, lens, with_lse, torch.full((B, Hkv, T), old, device=DEV), 0.0)
+        for b in range(B):
+            n = T if lens is None else lens[b]
+            assert torch.equal(got[b, :, :n], want[b, :, :n]) and torch.isfinite(got[b, :, :n]).all()
+            assert torch.equal(got[b, :, n:].isnan(), torch.full_like(got[b, :, n:], old).isnan())  # left alone
+
+
 def test_weights_follow_their_keys_through_eviction():
     """Steps of a bounded cache: the accumulated weight of every key against the
     64-bit sum over that key's own logits and statistics, where it started and
