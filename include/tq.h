@@ -387,8 +387,8 @@ TQ_API tq_status tq_attend_prefix(const tq_codec *kc, const tq_codec *vc,
  *   lens     device [B] int32 as in tq_attend_prefix; NULL: all T
  *   lse      [B][Hq] fp32: the softmax's statistic over all of the row's keys,
  *            such as tq_attend_prefix's lse when there is a shared prefix;
- *            -inf adds nothing.  NULL: the softmax over the row's own lens[b]
- *            keys; a row whose logits are all -inf adds nothing
+ *            -inf and +inf add nothing.  NULL: the softmax over the row's own
+ *            lens[b] keys; a row whose logits are all -inf adds nothing
  *   scale    0 -> 1/sqrt(d) of kc
  *   decay    finite; 1 keeps the sum, less than 1 lets old weight fade, 0 starts
  *            anew: the old content of mass is then not read

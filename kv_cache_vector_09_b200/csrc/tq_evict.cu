@@ -61,10 +61,12 @@ __global__ void __launch_bounds__(256)
   const int64_t bh = blockIdx.x / pieces, t0 = blockIdx.x % pieces * kGivenKeys;
   const int h = (int)(bh % Hkv), b = (int)(bh / Hkv), G = Hq / Hkv;
   if (threadIdx.x < G) {
-    // ln to log2 units, in two parts; a row without keys gives nothing: 2^(x - inf) = 0
+    // ln to log2 units, in two parts; a row without keys gives nothing, nor does
+    // one whose sum is infinite: 2^(x - inf) = 0
     const double stat = (double)lse[b * Hq + h * G + threadIdx.x] * 1.4426950408889634;
-    s_hi[threadIdx.x] = stat == -INFINITY ? INFINITY : (float)stat;
-    s_lo[threadIdx.x] = stat == -INFINITY ? 0.f : (float)(stat - (double)(float)stat);
+    const float hi = stat == -INFINITY ? INFINITY : (float)stat;  // infinite beyond fp32 too
+    s_hi[threadIdx.x] = hi;
+    s_lo[threadIdx.x] = isinf(hi) ? 0.f : (float)(stat - (double)hi);
   }
   const int64_t n = held_len(lens, b, T, p.err);
   if (t0 >= n) return;

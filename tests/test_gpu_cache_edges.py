@@ -84,6 +84,17 @@ def test_a_decay_of_zero_forgets_the_old_weight(B, Hq, Hkv, T, lens, with_lse):
             assert torch.equal(got[b, :, n:].isnan(), torch.full_like(got[b, :, n:], old).isnan())  # left alone
 
 
+@pytest.mark.parametrize("T", [8, 4097])
+def test_a_statistic_of_infinity_adds_nothing(T):
+    # e^(l - inf) = 0, as for a row without keys; 3e38 log2(e) is beyond fp32
+    lse = torch.tensor([[math.inf, -math.inf, 9.0, 3e38]], device=DEV)
+    logits = torch.randn((1, 4, T), generator=torch.Generator().manual_seed(T)).to(DEV) * 20.0
+    got = weights(1, 4, 2, T, None, True, torch.ones((1, 2, T), device=DEV), 0.5, logits, lse)
+    assert torch.all(got[0, 0] == 0.5)
+    p = torch.exp(logits[0, 2].double() / math.sqrt(128) - 9.0)
+    assert torch.all((got[0, 1].double() - 0.5 - p).abs() <= U * (1 + 40 * p))  # |exponent| <= 20: 20 u, exp2 4 u
+
+
 def test_weights_follow_their_keys_through_eviction():
     """Steps of a bounded cache: the accumulated weight of every key against the
     64-bit sum over that key's own logits and statistics, where it started and
