@@ -33,8 +33,8 @@ __device__ __forceinline__ int64_t held_len(const int32_t* lens, int b, int64_t 
 struct Exponent {
   float ch, cl;  // scale * log2(e)
   __device__ __forceinline__ float of(float l, float hi, float lo) const {  // l * c - (hi + lo)
-    l = l == -INFINITY ? -3.4028235e38f : l;  // a masked key: -inf * cl could be +inf or NaN
-    return fmaf(l, cl, fmaf(l, ch, -hi) - lo);
+    // a masked key: -inf * cl could be +inf or NaN
+    return fabsf(l) == INFINITY ? l - hi : fmaf(l, cl, fmaf(l, ch, -hi) - lo);
   }
 };
 

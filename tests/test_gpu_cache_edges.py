@@ -95,6 +95,21 @@ def test_a_statistic_of_infinity_adds_nothing(T):
     assert torch.all((got[0, 1].double() - 0.5 - p).abs() <= U * (1 + 40 * p))  # |exponent| <= 20: 20 u, exp2 4 u
 
 
+@pytest.mark.parametrize("T", [8, 4097])
+def test_infinite_logits_follow_the_definition(T):
+    # e^(-inf) = 0 at every scale, and e^(inf) = inf
+    lse = torch.zeros((1, 2), device=DEV)
+    for scale in (1e-38, 0.5, 64.0):
+        logits = torch.zeros((1, 2, T), device=DEV)
+        logits[0, :, 0::3] = -math.inf
+        logits[0, 0, 1] = math.inf
+        got = weights(1, 2, 2, T, None, True, torch.ones((1, 2, T), device=DEV), 1.0, logits, lse, scale)
+        want = torch.full((2, T), 2.0, device=DEV)
+        want[:, 0::3] = 1.0
+        want[0, 1] = math.inf
+        assert torch.equal(got[0], want), scale
+
+
 def test_weights_follow_their_keys_through_eviction():
     """Steps of a bounded cache: the accumulated weight of every key against the
     64-bit sum over that key's own logits and statistics, where it started and
