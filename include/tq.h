@@ -366,9 +366,13 @@ TQ_API tq_status tq_attend_prefix_workspace_size(const tq_codec *kc,
  * The result of a call does not depend on other calls, and the same call gives
  * the same bits.  Logits, the exponentials' sums and the weighted values are
  * accumulated in fp32, from operands good to 2^-22; out_dtype only rounds the
- * result, and lse does not change it.  d <= 256, Hq / Hkv <= 32, a value sketch
- * of m <= 128 (else TQ_ERR_UNSUPPORTED).  workspace: 16-byte aligned; calls that
- * may overlap on the GPU need one each.                                      */
+ * result, and lse does not change it.  One bound more where a value's norm is
+ * far below its neighbours': weight times norm, the row's largest weight being
+ * 1, is good to 2^-37 of the largest norm among 64 consecutive values, so that
+ * beside a norm 2^15 times larger it still has its 2^-22, beside 2^20 times
+ * 2^-17.  d <= 256, Hq / Hkv <= 32, a value sketch of m <= 128 (else
+ * TQ_ERR_UNSUPPORTED).  workspace: 16-byte aligned; calls that may overlap on
+ * the GPU need one each.                                                     */
 TQ_API tq_status tq_attend_prefix(const tq_codec *kc, const tq_codec *vc,
                     const void *q, tq_dtype dtype, int B, int Hq, int Hkv,
                     float scale, int64_t Tp, const tq_compressed *Kp,

@@ -17,7 +17,9 @@
 //   P = 2^(l - M) nu_v 2^(14 - e) as fp16, back into TMEM over S,
 //   O = P c_v into TMEM, added into acc in registers with the weight 2^(e - 14).
 // 2^e bounds the tile's value norms, so that P uses fp16's range whatever the
-// norms; O starts from zero each tile, so that the tensor core's truncating
+// norms; its parts end at fp16's 2^-24, so a weighted norm is good to 2^-37 of
+// the tile's largest norm where that is more than 2^-22 of itself (a scale by
+// the row's largest product would need its maximum exchanged too).  O starts from zero each tile, so that the tensor core's truncating
 // accumulation only ever spans one tile.
 //
 // Operands are two fp16 parts each (x = hi + lo, 2^-22 relative) and a product

@@ -176,3 +176,30 @@ def test_the_result_is_one_value_rounded_to_its_type(case):
             out, l = g.run(odt, with_lse)
             assert torch.equal(out, want.to(odt)), (odt, with_lse)
             assert l is None or torch.equal(l, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,m", [(128, 128), (64, 0)])
+@pytest.mark.parametrize("power", [10, 15, 20, 28])
+def test_values_beside_a_norm_far_above_theirs(d, m, power):
+    # in the tile of the heaviest key, a value of 2^power times the norm whose own key weighs nothing
+    ks, vs = dict(bits=(3,), m=m), dict(bits=(4,), seed=4)
+    case = (d, ks, vs, 1, 1, 1, 500, 0, [0], FL, 1.0, 4.0)
+    p = Problem(*case)
+    k = p.kc.coord_cen(O.unpack_codes(p.Kp.codes, p.kc)) / math.sqrt(d)
+    if m:
+        gam = p.Kp.rnorms.astype(np.float64)[:, None] * math.sqrt(math.pi / 2) / m
+        k = k + gam * ((2.0 * O.unpack_bits(p.Kp.signs, m) - 1.0) @ p.kc.S.astype(np.float64))
+    l = (k * p.Kp.norms.astype(np.float64)[:, None]) @ (p.kc.Pi @ p.q[0, 0].double().numpy())
+    tile = np.arange(500) // 64
+    near = np.flatnonzero(tile == tile[l.argmax()])
+    far = near[l[near].argmin()]
+    assert l[far] - l.max() < -(28 + 30) * math.log(2)
+    p.Vp.norms[far] = 3.0 * 2.0 ** power
+    o, s, eo, _ = p.solve()
+    e, nv = np.exp(l - l.max()), p.Vp.norms.astype(np.float64)
+    top = np.array([nv[tile == t].max() for t in range(tile.max() + 1)])[tile]
+    lost = np.minimum(2.0 ** -37 * top, e * nv)
+    eo = eo - LAM * math.sqrt(500) * 2.0 ** -37 * nv.max() + LAM * math.sqrt((lost * lost).sum()) / e.sum()
+    out, _ = Device(p, ks, vs).run(FL, True)
+    assert ratio(np.linalg.norm(out.double().cpu().numpy() - o, axis=-1), eo) <= 1
