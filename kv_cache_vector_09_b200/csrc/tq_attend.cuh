@@ -480,7 +480,7 @@ cudaError_t launch_attend_q(const tq_params& kp, const tq_params& vp, const floa
   const size_t smem = sizeof(float) * (size_t)lay.total;
   if (smem > 200 * 1024) return cudaErrorNotSupported;
   auto fn = attend_kernel<D, NG, KB0, KB1, VQ>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = tq_allow_smem((const void*)fn, smem);
   if (e != cudaSuccess) return e;
   const int G = Hq / Hkv, nsub = (G + NG - 1) / NG;
   dim3 grid((unsigned)nchunk, (unsigned)(Hkv * nsub), (unsigned)B);

@@ -731,6 +731,23 @@ static tq_status check_compressed(const tq_codec* c, const tq_compressed* t, con
   return TQ_OK;
 }
 
+cudaError_t tq_allow_smem(const void* fn, size_t bytes) {
+  static std::mutex mu;
+  static std::map<std::pair<const void*, int>, size_t> limits;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  size_t& limit = limits[{fn, dev}];
+  const size_t want = std::max(limit, bytes);
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)want);
+  if (e == cudaSuccess)
+    limit = want;
+  else
+    cudaGetLastError();  // returned here, not by the next launch
+  return e;
+}
+
 static tq_status launch_status(cudaError_t e, const char* what) {
   if (e != cudaSuccess) return cuda_fail(e, what);
   return TQ_OK;

@@ -105,6 +105,11 @@ struct tq_codec {
 void tq_set_error(const char* fmt, ...);
 tq_status tq_fail(tq_status st, const char* fmt, ...);
 
+// Raises a kernel's limit of dynamic shared memory on the current device to at
+// least `bytes`.  The limit is the process's and is never lowered, so that a
+// launch on one host thread does not depend on what another thread launches.
+cudaError_t tq_allow_smem(const void* fn, size_t bytes);
+
 // launchers implemented in the .cu files; arguments already validated
 cudaError_t tq_launch_quantize(const tq_params& p, const void* x, tq_dtype dt, int64_t n, int64_t ld,
                                const tq_compressed& out, cudaStream_t st);

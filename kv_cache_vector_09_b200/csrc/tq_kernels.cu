@@ -780,7 +780,7 @@ int num_sms() {
 
 template <typename Fn>
 cudaError_t set_smem(Fn* fn, size_t bytes) {
-  if (bytes > 48 * 1024) return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (bytes > 48 * 1024) return tq_allow_smem((const void*)fn, bytes);
   return cudaSuccess;
 }
 

@@ -856,7 +856,7 @@ cudaError_t launch_quad(const tq_params& p, const void* x, int64_t n, int64_t ld
   const int m = SK ? p.m : 0;
   const QLayout ly(D, m, W, NT / 32);
   auto fn = tq_quantize_quad_kernel<D, B0, B1, SK, TIn, ROPE>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ly.total);
+  cudaError_t e = tq_allow_smem((const void*)fn, ly.total);
   if (e != cudaSuccess) return e;
   uint32_t cols = 32;  // accumulator: 2m columns when the sketch uses the merged N = 2m product
   if constexpr (SK) {

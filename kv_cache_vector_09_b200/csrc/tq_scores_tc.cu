@@ -746,7 +746,7 @@ cudaError_t launch_scores_t(const tq_params& p, const tq_compressed& K, float* l
   // shared memory so that a second block never waits on the allocation
   smem = std::max(smem, (size_t)(smem_per_sm() / 2 + 1024));
   auto fn = tq_scores_tc_kernel<D, B0, B1, RING, NI>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = tq_allow_smem((const void*)fn, smem);
   if (e != cudaSuccess) return e;
   const int64_t tpg = (T + kKeys - 1) / kKeys;
   const int64_t ntiles = (int64_t)B * Hkv * tpg;
@@ -803,8 +803,7 @@ cudaError_t tq_launch_scores_tc(const tq_params& p, const float* qprep, int B, i
   uint8_t* ws = reinterpret_cast<uint8_t*>(ws_tc);
   const size_t smem = sizeof(float) * (size_t)(Hq / Hkv) * (p.d + p.m);
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(tq_scores_bbuild_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem);
+    const cudaError_t e = tq_allow_smem((const void*)tq_scores_bbuild_kernel, smem);
     if (e != cudaSuccess) return e;
   }
   tq_scores_bbuild_kernel<<<dim3((unsigned)(B * Hkv), 8), 256, smem, st>>>(p, qprep, Hq, Hkv, ws);

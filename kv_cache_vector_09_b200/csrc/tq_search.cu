@@ -793,7 +793,7 @@ cudaError_t tq_launch_search(const tq_params& p, const float* qprep, int nq, int
 #define TQ_SEARCH_CASE(B)                                                                                  \
   case B: {                                                                                                \
     auto fn = search_kernel<B>;                                                                            \
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);                  \
+    e = tq_allow_smem((const void*)fn, smem);                                                              \
     if (e != cudaSuccess) return e;                                                                        \
     fn<<<grid, kThreads, smem, st>>>(p, a);                                                                \
     break;                                                                                                 \
