@@ -257,7 +257,8 @@ TQ_API tq_status tq_rope_cache(double theta, int d, int max_pos, float *cos_sin,
  * rope->positions[i] before normalisation.  A position outside [0, max_pos)
  * is replaced by 0 and recorded as code 3 in the codec's device error word
  * (tq_codec_device_error).  Requires d = 64 or 128, TQ_BF16 or TQ_F32 rows,
- * m <= 256, scalar codes and the Hadamard rotation (else TQ_ERR_UNSUPPORTED). */
+ * m <= 256 (d = 128: m <= 224), scalar codes and the Hadamard rotation (else
+ * TQ_ERR_UNSUPPORTED).                                                       */
 TQ_API tq_status tq_quantize_rope(const tq_codec *codec, const void *x, tq_dtype dtype,
                                   int64_t n, int64_t ld, const tq_rope *rope,
                                   const tq_compressed *out, void *stream);

@@ -820,7 +820,7 @@ extern "C" tq_status tq_quantize_rope(const tq_codec* c, const void* x, tq_dtype
   p.rope_max_pos = rope->max_pos;
   const cudaError_t e = tq_launch_quantize_tc_rope(p, x, dt, n, ld, *out, (cudaStream_t)stream);
   if (e == cudaErrorNotSupported)
-    return tq_fail(TQ_ERR_UNSUPPORTED, "tq_quantize_rope: needs d of 64 or 128, bf16 or fp32 rows and m <= 256");
+    return tq_fail(TQ_ERR_UNSUPPORTED, "tq_quantize_rope: needs d of 64 or 128, bf16 or fp32 rows and m <= 256 (d = 128: 224)");
   return launch_status(e, "tq_quantize_rope launch");
 }
 
@@ -851,7 +851,7 @@ extern "C" tq_status tq_append(const tq_codec* c, const void* x, tq_dtype dt, in
     p.rope_max_pos = rope->max_pos;
     e = tq_launch_quantize_tc_rope(p, x, dt, rows, ld, *cache, (cudaStream_t)stream);
     if (e == cudaErrorNotSupported)
-      return tq_fail(TQ_ERR_UNSUPPORTED, "tq_append with RoPE: needs d of 64 or 128, bf16 or fp32 rows and m <= 256");
+      return tq_fail(TQ_ERR_UNSUPPORTED, "tq_append with RoPE: needs d of 64 or 128, bf16 or fp32 rows and m <= 256 (d = 128: 224)");
   } else {
     e = tq_launch_quantize_tc(p, x, dt, rows, ld, *cache, (cudaStream_t)stream);
     if (e == cudaErrorNotSupported) e = tq_launch_quantize(p, x, dt, rows, ld, *cache, (cudaStream_t)stream);

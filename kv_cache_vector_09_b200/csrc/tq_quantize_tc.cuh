@@ -857,6 +857,8 @@ cudaError_t launch_quad(const tq_params& p, const void* x, int64_t n, int64_t ld
   const QLayout ly(D, m, W, NT / 32);
   auto fn = tq_quantize_quad_kernel<D, B0, B1, SK, TIn, ROPE>;
   cudaError_t e = tq_allow_smem((const void*)fn, ly.total);
+  // more than a block has (d = 128 with m = 256): the CUDA-core encoder's
+  if (e == cudaErrorInvalidValue) return cudaErrorNotSupported;
   if (e != cudaSuccess) return e;
   uint32_t cols = 32;  // accumulator: 2m columns when the sketch uses the merged N = 2m product
   if constexpr (SK) {
