@@ -177,3 +177,58 @@ def test_weights_follow_their_keys_through_eviction():
             a[..., :keep] = moved
     assert cuts >= 2
     assert tq.tq_codec_device_error(kc) == 0 and tq.tq_codec_device_error(vc) == 0
+
+
+def test_a_captured_step_replays_like_the_eager_one():
+    """Append, attention, scores, weights, choice and copies of one step in a
+    graph, replayed with other queries, lengths and contents."""
+    d, B, Hq, Hkv, Tp, T, keep = 128, 3, 8, 2, 100, 2100, 600
+    R = B * Hkv
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    f = lambda *s: 3.0 * torch.randn(s, generator=g, device=DEV)  # noqa: E731
+    kc, vc = tq.Codec(d, (3,), 128, 0), tq.Codec(d, (4,), 0, 1)
+    new = lambda n: [tq.tq_quantize(c, f(n, d), tq.Compressed.empty(c, n)) for c in (kc, vc)]  # noqa: E731
+    pre, own, kept, row = new(Hkv * Tp), new(R * T), new(R * keep), new(R)
+    x, q = [f(R, d) for _ in range(2)], f(B, Hq, d)
+    lens, at = torch.zeros(B, dtype=torch.int32, device=DEV), torch.zeros(R, dtype=torch.int32, device=DEV)
+    mass = torch.zeros((B, Hkv, T), device=DEV)
+    out, lse, logits = (torch.zeros(s, device=DEV) for s in ((B, Hq, d), (B, Hq), (B, Hq, T)))
+    idx = torch.zeros((B, Hkv, keep), dtype=torch.int32, device=DEV)
+    mass2, lens2 = torch.zeros((B, Hkv, keep), device=DEV), torch.zeros_like(lens)
+    ws = tq.workspace(tq.tq_attend_prefix_workspace_size(kc, vc, B, Hq, Hkv, Tp, T), DEV)
+    ws2 = tq.workspace(tq.tq_scores_workspace_size(kc, B, Hq, Hkv), DEV)
+    state = [t for c in own + kept for t in (c.codes, c.signs, c.norms, c.rnorms) if t is not None]
+    state += [mass, out, lse, idx, mass2, lens2]
+
+    def step():
+        for c, v, r, cache in zip((kc, vc), x, row, own):
+            tq.tq_quantize(c, v, r)
+            tq.tq_copy_rows(c, r, 1, cache, T, R, 1, dst_idx=at)
+        tq.tq_attend_prefix(kc, vc, q, B, Hq, Hkv, Tp, *pre, T, *own, out, ws, lens=lens, lse=lse)
+        tq.tq_scores(kc, q, B, Hq, Hkv, T, own[0], logits, ws2)
+        tq.tq_mass_update(kc, logits, B, Hq, Hkv, T, mass, lens=lens, lse=lse)
+        tq.tq_mass_update(kc, logits, B, Hq, Hkv, T, mass, lens=lens, decay=0.5)
+        tq.tq_evict_select(kc, mass, B, Hkv, T, keep, idx, lens=lens, sink=2, recent=9, mass_out=mass2, lens_out=lens2)
+        for c, a, z in zip((kc, vc), own, kept):
+            tq.tq_copy_rows(c, a, T, z, keep, R, keep, src_idx=idx)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n in ([5, 1, 2100], [2100, 601, 600], [1, 1, 1]):
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        at.copy_((lens - 1).repeat_interleave(Hkv))
+        q.copy_(f(B, Hq, d))
+        for v in x:
+            v.copy_(f(R, d))
+        before = [t.clone() for t in state]
+        step()
+        want = [t.clone() for t in state]
+        for t, b in zip(state, before):
+            t.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(state, want)), n
+    assert tq.tq_codec_device_error(kc) == 0 and tq.tq_codec_device_error(vc) == 0
