@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(256)
     for (int k = lane; k < D; k += 32) mx = fmaxf(mx, fabsf(qt[k][i]));
     for (int k = lane; k < m; k += 32) mx = fmaxf(mx, fabsf(wt[k][i]));
     mx = tq_warp_max(mx);
-    const int ex = mx > 0.f && mx < INFINITY ? max(-100, min(100, exponent_of(mx))) : 9;
+    // 2^(9 - ex) and 2^(ex - 9) are normal numbers
+    const int ex = mx > 0.f && mx < INFINITY ? max(-117, exponent_of(mx)) : 9;
     if (lane == 0) {
       s_up[i] = pow2(9 - ex);
       scales[(size_t)grp * kRows + r0 + i] = pow2(ex - 9);

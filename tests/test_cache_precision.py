@@ -203,3 +203,18 @@ def test_values_beside_a_norm_far_above_theirs(d, m, power):
     eo = eo - LAM * math.sqrt(500) * 2.0 ** -37 * nv.max() + LAM * math.sqrt((lost * lost).sum()) / e.sum()
     out, _ = Device(p, ks, vs).run(FL, True)
     assert ratio(np.linalg.norm(out.double().cpu().numpy() - o, axis=-1), eo) <= 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,m", [(128, 128), (64, 0)])
+@pytest.mark.parametrize("power", [-105, 105])
+def test_powers_of_two_pass_from_queries_to_keys(d, m, power):
+    # q 2^k against norms 2^-k are the same logits, bit for bit: every scale is a power of two
+    ks, vs = dict(bits=(3,), m=m), dict(bits=(4,), seed=4)
+    p = Problem(d, ks, vs, 3, 8, 2, 300, 70, [70, 0, 33], FL, 0.0, 4.0)
+    want, lse = Device(p, ks, vs).run(FL, True)
+    p.q = p.q * 2.0 ** power
+    for r in (p.Kp, p.K):
+        r.norms *= np.float32(2.0 ** -power)
+    out, l = Device(p, ks, vs).run(FL, True)
+    assert torch.isfinite(want).all() and torch.equal(out, want) and torch.equal(l, lse)
