@@ -58,10 +58,10 @@ STAGE_SOURCES = {
     "tq_attend": ("tq_attend.cuh", "tq_attend_d128.cu", "tq_attend_d64.cu", "tq_kernels.cu"),
 }
 TRAFFIC = {  # stage: (bytes per launch, sources digest)
-    "tq_quantize_K": (548_033_280 + 136_723_200, "60e1ebbf677f89535dcffe2d2e5732a96716f1153a8dd5f4d08bd95e315f0e4e"),
-    "tq_quantize_V": (539_169_536 + 124_970_752, "60e1ebbf677f89535dcffe2d2e5732a96716f1153a8dd5f4d08bd95e315f0e4e"),
-    "tq_scores": (152_425_216 + 16_209_152, "228a807d7a83dc7d46a04fb633a2a4483725173af5db74ea1b9696cc43088932"),
-    "tq_attend": (294_011_648 + 1_265_408, "6f14879f48fe4937f67c34bdc801060ae9d7e9b9ef2b97183262a81c333d1867"),
+    "tq_quantize_K": (547_958_016 + 137_107_712, "19da2c68545acc4c003c3342e251339b6d54ca06332f88547411e62d47ba23dd"),
+    "tq_quantize_V": (539_153_920 + 124_738_048, "19da2c68545acc4c003c3342e251339b6d54ca06332f88547411e62d47ba23dd"),
+    "tq_scores": (152_423_680 + 16_238_080, "2abc4eb301c743cf3e50ce35c76801f5380568abe80da8757137c9f370f26822"),
+    "tq_attend": (294_024_704 + 1_981_184, "bbd8b45cac757f2c2e4a0f586e352c70111c467481b91fdd8ee7fcf143f1cd31"),
 }
 
 

@@ -2,9 +2,11 @@
 // keys that stay, and the copy of their compressed records.
 //
 // Measured (B200): weights of 8 sequences, 32 heads, up to 32,768 keys (20 M
-// logits) 17.7 us where reading and writing them is 4.6; the choice of 8192 of up
-// to 32,768 keys for 64 rows 36 us, bound by the instructions per key and round;
-// the copies of its records 4.0 (keys) and 4.2 TB/s (values).
+// logits) 17.5 us where reading and writing them is 4.6, bound by latency and a
+// second wave of clusters; the choice of 8192 of up to 32,768 keys for 64 rows
+// 36 us, bound by latency (issue slots 32% in use: reads, barriers and the three
+// rounds); the copies of its records 4.0 (keys) and 4.2 TB/s (values), 1.28 times
+// that in sectors.
 #include <math.h>
 
 #include <algorithm>
@@ -298,7 +300,8 @@ __device__ __forceinline__ int before_warp(const int* s, int warp, int lane) {
 // sums the counters of all.  Then every warp counts what stays in its
 // contiguous piece, and after one scan over warps and blocks writes it in order.
 // The masses are read once and kept as ordered keys in shared memory when they
-// fit (KEEP).  Bound by the instructions per key, hence the 16-byte reads.
+// fit (KEEP).  Bound by latency; 16-byte reads of the counters (4-byte: 54 us
+// against 36) and of the keys leave fewer trips.
 template <bool KEEP>
 __global__ void __launch_bounds__(kEvThreads)
     evict_kernel(const tq_params p, const float* __restrict__ mass, const int Hkv, const int64_t T,

@@ -27,7 +27,7 @@
 // the result's type: one part (2^-11) would move a logit by its size times
 // 2^-11, and a weight by e to that, which at logits of 100 is twice a bf16
 // result's half step (32 sequences over 32,768 keys: 0.119 ms with one part,
-// 0.135 with two).
+// 0.136 with two).
 //
 // Operand bytes come from byte permutes: a code of up to three bits is a prmt
 // selector into the eight low or high bytes of the codebook's fp16 values; the
@@ -43,8 +43,8 @@
 // unrolling stay loops: all unrolled, a tile took up to 6300 cycles.
 //
 // Measured (B200, d = 128, 8 KV heads, 32 query heads, 3-bit keys with m = 128,
-// 4-bit values): 32 sequences over 32,768 + up to 1024 keys, bf16, 0.135 ms (196
-// TFLOP/s); 64 over 16,411 + up to 777, fp32 with statistics, 0.168 ms.  Bound by
+// 4-bit values): 32 sequences over 32,768 + up to 1024 keys, bf16, 0.136 ms (193
+// TFLOP/s); 64 over 16,411 + up to 777, fp32 with statistics, 0.166 ms.  Bound by
 // the latency of one tile's chain through its warps, about 3500 cycles for 2300 of
 // tensor-core time; reading the records is 9 us of it.
 #include <math.h>
